@@ -21,6 +21,7 @@ TW_ERR_CUDA = 4
 TW_ERR_TIMEOUT = 5
 
 c_i32 = ctypes.c_int32
+c_i64 = ctypes.c_int64
 c_vp = ctypes.c_void_p
 c_size = ctypes.c_size_t
 
@@ -72,6 +73,14 @@ _SIGS = {
     "tw_topp_prune_tokens": (ctypes.c_int, [c_vp, c_i32, ctypes.POINTER(TwKv), c_vp, c_vp, c_vp,
                                             c_vp, c_i32, c_vp, ctypes.c_double, c_i32, c_vp,
                                             c_i32, c_vp, c_vp, c_size, c_vp]),
+    "tw_update_page_table": (ctypes.c_int, [c_i32, c_vp, c_vp, c_vp, c_i32, c_i32, c_vp, c_i32,
+                                            c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp]),
+    "tw_write_rows": (ctypes.c_int, [ctypes.POINTER(TwKv), c_vp, c_i64, c_vp, c_i64, c_vp, c_i32,
+                                     c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "tw_prefix_workspace_size": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32,
+                                                ctypes.POINTER(c_size)]),
+    "tw_prefix_decode": (ctypes.c_int, [c_vp, c_i32, ctypes.POINTER(TwKv), c_i32, c_vp, c_vp, c_vp,
+                                        c_size, c_vp]),
     "tw_decode_step": (ctypes.c_int, [ctypes.POINTER(TwStep), c_vp]),
     "tw_decode_step_host": (ctypes.c_int, [ctypes.POINTER(TwStep), c_vp, c_vp, c_vp]),
     "tw_decode_step_num_kernels": (ctypes.c_int, [ctypes.POINTER(TwStep)]),

@@ -13,6 +13,7 @@ survivors.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 from typing import Optional
@@ -578,3 +579,195 @@ class LabelDecodeStep:
         self(self._q_stage, stream)
         out_host.copy_(self.out, non_blocking=True)
         return out_host
+
+
+# ----------------------------------------------------------------------------- serving around the cache
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """Make `device`, and `stream` if one is given, current: what is allocated
+    inside belongs to the stream the kernels run on."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device)
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def _need_on(t: torch.Tensor, dtype, name: str, device, shape=None):
+    _need(t, dtype, name)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+class PageTableUpdate:
+    """Page tables and slot maps on the GPU from request lengths
+    (tw_update_page_table), with output buffers for repeated calls.
+
+    seq_lens [B] are the lengths before the step, page_table [B][W] and the
+    stack free_pages [pool pages] are updated in place; the first prefix_len /
+    16 entries of every row are the caller's (a shared prefix).  A call takes
+    new_lens [B] and num_free [1] (all int32 CUDA tensors) and fills
+    seq_lens_out [B] (the lengths reached: a growth that finds no pages is
+    refused), num_free_out [1], slots [num_slots] (the cache slot of every new
+    token, -1 where there is none) and offsets [B + 1] (a sequence's first
+    place in slots).  in_place: seq_lens and num_free take the results
+    themselves (the names above are then the same tensors), so that a captured
+    call can be replayed step after step."""
+
+    def __init__(self, seq_lens: torch.Tensor, page_table: torch.Tensor,
+                 free_pages: torch.Tensor, num_slots: int = 0, prefix_len: int = 0,
+                 in_place: bool = False):
+        _need(seq_lens, torch.int32, "seq_lens")
+        dev = self.device = seq_lens.device
+        if seq_lens.dim() != 1 or page_table.dim() != 2 or free_pages.dim() != 1:
+            raise ValueError("seq_lens must be [B], page_table [B][W], free_pages [pool pages]")
+        B = int(seq_lens.shape[0])
+        _need_on(page_table, torch.int32, "page_table", dev, (B, page_table.shape[1]))
+        _need_on(free_pages, torch.int32, "free_pages", dev)
+        if num_slots < 0:
+            raise ValueError("num_slots must not be negative")
+        self.seq_lens, self.page_table, self.free_pages = seq_lens, page_table, free_pages
+        self.prefix_len, self.in_place, self.num_slots = int(prefix_len), bool(in_place), int(num_slots)
+        with torch.cuda.device(dev):
+            self.seq_lens_out = seq_lens if in_place else torch.empty_like(seq_lens)
+            self.num_free_out = None if in_place else seq_lens.new_zeros(1)
+            self.slots = seq_lens.new_full((num_slots,), -1)
+            self.offsets = seq_lens.new_zeros(B + 1)
+
+    def __call__(self, new_lens: torch.Tensor, num_free: torch.Tensor,
+                 stream=None) -> "PageTableUpdate":
+        lib = _capi.load()
+        B, W = self.page_table.shape
+        _need_on(new_lens, torch.int32, "new_lens", self.device, (B,))
+        _need_on(num_free, torch.int32, "num_free", self.device, (1,))
+        if self.in_place:
+            self.num_free_out = num_free
+        with _on(self.device, stream) as st:
+            check(lib.tw_update_page_table(
+                B, _ptr(self.seq_lens), _ptr(new_lens), _ptr(self.page_table), W, self.prefix_len,
+                _ptr(self.free_pages), self.free_pages.shape[0], _ptr(num_free),
+                _ptr(self.num_free_out), _ptr(self.seq_lens_out),
+                _ptr(self.slots) if self.num_slots else None, self.num_slots, _ptr(self.offsets),
+                st.cuda_stream), "tw_update_page_table")
+        return self
+
+
+def update_page_table(seq_lens: torch.Tensor, new_lens: torch.Tensor, page_table: torch.Tensor,
+                      free_pages: torch.Tensor, num_free: torch.Tensor, num_slots: int = 0,
+                      prefix_len: int = 0, stream=None) -> PageTableUpdate:
+    """One PageTableUpdate call with new output buffers: its seq_lens_out,
+    num_free_out, slots and offsets are the results."""
+    with _on(seq_lens.device, stream):
+        u = PageTableUpdate(seq_lens, page_table, free_pages, num_slots, prefix_len)
+    return u(new_lens, num_free, stream)
+
+
+def _token_rows(t: torch.Tensor, name: str, kv: KVCache, T: int) -> int:
+    """Check new rows [T][Hk][128] (a slice of a wider projection may be given:
+    only the last two dimensions must be packed).  Returns the token stride."""
+    if t.dtype != torch.float16 or t.device != kv.k.device or \
+            tuple(t.shape) != (T, kv.Hk, HEAD_DIM):
+        raise ValueError(f"{name} must be fp16 [{T}][{kv.Hk}][128] on {kv.k.device}")
+    if t.stride(2) != 1 or (kv.Hk > 1 and t.stride(1) != HEAD_DIM):
+        raise ValueError(f"{name}: a token's heads must lie side by side")
+    stride = t.stride(0) if T > 1 else kv.Hk * HEAD_DIM
+    if stride < kv.Hk * HEAD_DIM or stride % 8:
+        raise ValueError(f"{name}: token stride {stride} must be a multiple of 8, "
+                         f"at least {kv.Hk * HEAD_DIM}")
+    return stride
+
+
+def write_rows(kv: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
+               keys: Optional[Int4Keys] = None, meta: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """Write new K / V rows [T][Hk][128] to the cache slots slots [T] (int32, -1
+    skips) and, in the same pass, quantise the keys into `keys` and fold them
+    into `meta` (if given): tw_write_rows."""
+    lib = _capi.load()
+    dev = kv.k.device
+    if kv.v is None:
+        raise ValueError("the cache has no v")
+    _need_on(slots, torch.int32, "slots", dev)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    T = int(slots.shape[0])
+    ks, vs = _token_rows(k_new, "k_new", kv, T), _token_rows(v_new, "v_new", kv, T)
+    if keys is not None:
+        _need_on(keys.codes, torch.uint8, "codes", dev)
+        _check_keys(kv, keys)
+        _need_on(keys.scales, torch.float16, "scales", dev, kv.row_shape(4))
+        _need_on(keys.zeros, torch.float16, "zeros", dev, kv.row_shape(4))
+    if meta is not None:
+        _need_on(meta, torch.float16, "meta", dev, kv.meta_shape())
+    if T == 0:
+        return
+    s = kv.struct()
+    with _on(dev, stream) as st:
+        check(lib.tw_write_rows(
+            ctypes.byref(s), _ptr(k_new), ks, _ptr(v_new), vs, _ptr(slots), T,
+            _ptr(keys.codes) if keys else None, _ptr(keys.scales) if keys else None,
+            _ptr(keys.zeros) if keys else None, _ptr(meta), st.cuda_stream), "tw_write_rows")
+
+
+def prefix_workspace_bytes(B: int, Hq: int, Hk: int, prefix_len: int) -> int:
+    lib = _capi.load()
+    n = ctypes.c_size_t(0)
+    check(lib.tw_prefix_workspace_size(B, Hq, Hk, prefix_len, ctypes.byref(n)),
+          "tw_prefix_workspace_size")
+    return int(n.value)
+
+
+class PrefixDecodeStep:
+    """Dense decode attention of a batch whose sequences share their first
+    prefix_len tokens (tw_prefix_decode), with pre-allocated outputs `out`
+    [B][Hq][128], `lse` [B][Hq] (or None) and workspace for repeated calls.
+
+    The shared tokens are read once, from sequence 0's first pages (or
+    contiguous rows).  prefix_len 0 shares nothing: plain dense decode."""
+
+    def __init__(self, kv: KVCache, Hq: int, prefix_len: int, with_lse: bool = True):
+        if kv.v is None:
+            raise ValueError("the cache has no v")
+        if prefix_len < 0 or prefix_len % PAGE or prefix_len > kv.N:
+            raise ValueError(f"prefix_len must be a multiple of {PAGE} in [0, {kv.N}]")
+        dev = kv.k.device
+        for t, name in ((kv.v, "v"), (kv.seq_lens, "seq_lens"), (kv.page_table, "page_table")):
+            if t is not None and t.device != dev:
+                raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        shape = (kv.page_table if kv.paged else kv.k).shape
+        if shape[0] != kv.B:
+            raise ValueError(f"the cache has {shape[0]} sequences, seq_lens {kv.B}")
+        self.kv, self.Hq, self.prefix_len = kv, int(Hq), int(prefix_len)
+        with torch.cuda.device(dev):
+            self.out = torch.zeros((kv.B, Hq, HEAD_DIM), dtype=torch.float16, device=dev)
+            self.lse = torch.zeros((kv.B, Hq), dtype=torch.float32, device=dev) if with_lse \
+                else None
+            n = max(prefix_workspace_bytes(kv.B, self.Hq, kv.Hk, self.prefix_len), 256)
+            self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            self.ws[:256].zero_()   # the device status word
+        self._kvs = kv.struct()
+
+    def __call__(self, q: torch.Tensor, stream=None) -> torch.Tensor:
+        lib = _capi.load()
+        _need_on(q, torch.float16, "q", self.kv.k.device, (self.kv.B, self.Hq, HEAD_DIM))
+        if self.kv.B == 0:
+            return self.out
+        with _on(self.kv.k.device, stream) as st:
+            check(lib.tw_prefix_decode(
+                _ptr(q), self.Hq, ctypes.byref(self._kvs), self.prefix_len, _ptr(self.out),
+                _ptr(self.lse), _ptr(self.ws), self.ws.numel(), st.cuda_stream),
+                "tw_prefix_decode")
+        return self.out
+
+
+def prefix_decode(q: torch.Tensor, kv: KVCache, prefix_len: int, with_lse: bool = True,
+                  stream=None):
+    """One PrefixDecodeStep call with new buffers: tw_prefix_decode -> (out, lse)."""
+    with _on(kv.k.device, stream):
+        step = PrefixDecodeStep(kv, int(q.shape[1]), prefix_len, with_lse)
+    return step(q, stream), step.lse

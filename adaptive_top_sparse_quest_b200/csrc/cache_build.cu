@@ -168,6 +168,131 @@ k_append_keys(Layout L, const __half* __restrict__ K, uint8_t* __restrict__ code
   griddep_launch();
 }
 
+// Write new K/V rows by slot.  Rows t of k_new / v_new go to the cache rows that
+// slots[t] names; in the same pass over the key row it is quantised, and the
+// page's min / max is folded, so K is read once instead of three times.
+//
+// A run of list neighbours on consecutive slots of one page is one half-warp's
+// work per KV head: it alone touches that page's metadata, so no atomics are
+// needed and the result does not depend on an order.  The run that starts at a
+// page's first row starts its metadata anew; another folds what is there (its
+// earlier rows are in it).  A block looks at `chunk` list places and takes the
+// runs that start there, to their ends up to 15 places further on.
+constexpr int kWrThreads = 256;
+constexpr int kWrRows = 4;   // rows of a run in flight per half-warp
+
+template <int BITS>
+__global__ void __launch_bounds__(kWrThreads)
+k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restrict__ v_new,
+             int64_t k_stride, int64_t v_stride, const int32_t* __restrict__ slots, int T,
+             int chunk, __half* __restrict__ K, __half* __restrict__ V,
+             uint8_t* __restrict__ codes, __half* __restrict__ scales, __half* __restrict__ zeros,
+             __half* __restrict__ meta) {
+  __shared__ int sl[kWrMaxChunk + kPage + 1];   // slots of places t0 - 1 .. t0 + chunk + 14
+  __shared__ int run_at[kWrMaxChunk], run_n[kWrMaxChunk];
+  __shared__ int nruns;
+  const int tid = threadIdx.x, lane = tid & 31, l16 = tid & 15;
+  const unsigned hmask = 0xFFFFu << (lane & 16);
+  const int64_t t0 = (int64_t)blockIdx.x * chunk;
+  const int nslot = L.page_table ? L.pool_pages * kPage : L.B * L.N;
+  if (tid < chunk + kPage) {
+    const int64_t t = t0 - 1 + tid;
+    const int s = t >= 0 && t < T ? slots[t] : -1;
+    sl[tid] = (unsigned)s < (unsigned)nslot ? s : -1;
+  }
+  if (tid == 0) nruns = 0;
+  __syncthreads();
+  // position of a slot within its sequence (paged: its pool page)
+  auto offset = [&](int s) { return L.page_table ? s % kPage : s % L.N; };
+  if (tid < chunk && sl[tid + 1] >= 0) {
+    const int s = sl[tid + 1], o = offset(s) % kPage;
+    const bool starts = o == 0 || sl[tid] != s - 1;
+    if (starts) {
+      // rows left in the page; a contiguous sequence may end before its page does
+      const int left = L.page_table ? kPage - o : min(kPage - o, L.N - offset(s));
+      int n = 1;
+      while (n < left && sl[tid + 1 + n] == s + n) ++n;
+      const int r = atomicAdd(&nruns, 1);   // the runs' order does not matter
+      run_at[r] = tid;
+      run_n[r] = n;
+    }
+  }
+  __syncthreads();
+  const int h0 = blockIdx.y * (kWrThreads / 16);
+  const int nh = min(kWrThreads / 16, L.Hk - h0);
+  for (int i = tid >> 4; i < nruns * nh; i += kWrThreads / 16) {
+    const int r = i / nh, h = h0 + i % nh;
+    const int n = run_n[r], s = sl[run_at[r] + 1];
+    const int64_t tok = t0 + run_at[r];
+    int64_t row, mrec;
+    int o;
+    if (L.page_table) {
+      o = s % kPage;
+      mrec = (int64_t)(s / kPage) * L.Hk + h;
+      row = mrec * kPage + o;
+    } else {
+      const int t = s % L.N;
+      o = t % kPage;
+      const int64_t bh = (int64_t)(s / L.N) * L.Hk + h;
+      row = bh * L.N + t;
+      mrec = bh * L.max_pages + t / kPage;
+    }
+    const __half* ks = k_new + tok * k_stride + h * kHeadDim + l16 * 8;
+    const __half* vs = v_new + tok * v_stride + h * kHeadDim + l16 * 8;
+    int kmin[8], kmax[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      kmin[j] = 0x7FFFFFFF;
+      kmax[j] = -0x7FFFFFFF - 1;
+    }
+    for (int c = 0; c < n; c += kWrRows) {
+      uint4 kr[kWrRows], vr[kWrRows];
+#pragma unroll
+      for (int x = 0; x < kWrRows; ++x)
+        if (c + x < n) {
+          kr[x] = ld_stream16(ks + (c + x) * k_stride);
+          vr[x] = ld_stream16(vs + (c + x) * v_stride);
+        }
+#pragma unroll
+      for (int x = 0; x < kWrRows; ++x)
+        if (c + x < n) {
+          const int64_t at = row + c + x;
+          *reinterpret_cast<uint4*>(K + at * kHeadDim + l16 * 8) = kr[x];
+          *reinterpret_cast<uint4*>(V + at * kHeadDim + l16 * 8) = vr[x];
+          if (codes) quantize_row<BITS>(kr[x], at, lane, hmask, codes, scales, zeros);
+          const uint32_t w[4] = {kr[x].x, kr[x].y, kr[x].z, kr[x].w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int kk = h_key((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+            kmin[j] = min(kmin[j], kk);
+            kmax[j] = max(kmax[j], kk);
+          }
+        }
+    }
+    if (!meta) continue;
+    __half* dst = meta + mrec * (2 * kHeadDim) + l16 * 8;
+    if (o != 0) {
+      const uint4 omn = *reinterpret_cast<const uint4*>(dst);
+      const uint4 omx = *reinterpret_cast<const uint4*>(dst + kHeadDim);
+      const uint32_t on[4] = {omn.x, omn.y, omn.z, omn.w};
+      const uint32_t ox[4] = {omx.x, omx.y, omx.z, omx.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        kmin[j] = min(kmin[j], h_key((on[j >> 1] >> (16 * (j & 1))) & 0xFFFFu));
+        kmax[j] = max(kmax[j], h_key((ox[j >> 1] >> (16 * (j & 1))) & 0xFFFFu));
+      }
+    }
+    uint32_t mn[4], mx[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      mn[j] = h_from_key(kmin[2 * j]) | (h_from_key(kmin[2 * j + 1]) << 16);
+      mx[j] = h_from_key(kmax[2 * j]) | (h_from_key(kmax[2 * j + 1]) << 16);
+    }
+    *reinterpret_cast<uint4*>(dst) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
+    *reinterpret_cast<uint4*>(dst + kHeadDim) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
+  }
+}
+
 __global__ void __launch_bounds__(256)
 k_page_meta(Layout L, const __half* __restrict__ K, __half* __restrict__ meta) {
   const int l16 = threadIdx.x & 15;
@@ -247,6 +372,20 @@ void launch_page_meta(const Layout& L, const __half* K, __half* meta, cudaStream
   const int64_t cap_blocks = (int64_t)num_sms * 8;
   const int blocks = (int)(want < 1 ? 1 : (want < cap_blocks ? want : cap_blocks));
   k_page_meta<<<blocks, 256, 0, st>>>(L, K, meta);
+}
+
+cudaError_t launch_write_rows(const Layout& L, const __half* k_new, const __half* v_new,
+                              int64_t k_stride, int64_t v_stride, const int32_t* slots, int T,
+                              __half* K, __half* V, uint8_t* codes, __half* scales, __half* zeros,
+                              __half* meta, cudaStream_t st, int num_sms) {
+  // list places per block: as many as a page has rows, fewer while the grid
+  // would not give every SM two blocks (single tokens are a run each)
+  int chunk = kWrMaxChunk;
+  while (chunk > 1 && (T + chunk - 1) / chunk < 2 * num_sms) chunk /= 2;
+  const dim3 grid((T + chunk - 1) / chunk, (L.Hk + kWrThreads / 16 - 1) / (kWrThreads / 16));
+  return launch_k(L.kbits == 2 ? k_write_rows<2> : k_write_rows<4>, grid, dim3(kWrThreads), 0, st,
+                  false, L, k_new, v_new, k_stride, v_stride, slots, T, chunk, K, V, codes, scales,
+                  zeros, meta);
 }
 
 }  // namespace tw

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include "twilight.h"
 #include "tw_kernels.h"
@@ -671,6 +672,111 @@ int tw_decode_step_profiled(const tw_step* step, void* const* events, int32_t n_
                             void* stream) {
   if (!events || n_events < tw_decode_step_num_kernels(step) + 1) return TW_ERR_INVALID_ARG;
   return decode_step_impl(step, events, n_events, static_cast<cudaStream_t>(stream));
+}
+
+int tw_update_page_table(int32_t batch, const int32_t* seq_lens, const int32_t* new_lens,
+                         int32_t* page_table, int32_t max_pages_per_seq, int32_t prefix_len,
+                         int32_t* free_pages, int32_t num_pool_pages, const int32_t* num_free,
+                         int32_t* num_free_out, int32_t* out_lens, int32_t* slots,
+                         int32_t num_slots, int32_t* offsets, void* stream) {
+  if (batch < 0 || max_pages_per_seq < 1 || num_pool_pages < 1 || num_slots < 0 ||
+      prefix_len < 0 || prefix_len % tw::kPage != 0 ||
+      prefix_len / tw::kPage > max_pages_per_seq)
+    return TW_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)free_pages, (const void*)num_free, (const void*)num_free_out,
+                        (const void*)offsets})
+    if (!p || !aligned(p, 4)) return TW_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)seq_lens, (const void*)new_lens, (const void*)page_table,
+                        (const void*)out_lens})   // may be null when there is no sequence
+    if ((!p && batch > 0) || !aligned(p, 4)) return TW_ERR_INVALID_ARG;
+  if (!aligned(slots, 4) || (!slots && num_slots != 0)) return TW_ERR_INVALID_ARG;
+  // page sums, positions and slots are 32-bit
+  if (batch > tw::kPtMaxBatch || (int64_t)batch * max_pages_per_seq > INT32_MAX ||
+      (int64_t)max_pages_per_seq * tw::kPage > INT32_MAX ||
+      (int64_t)num_pool_pages * tw::kPage > INT32_MAX)
+    return TW_ERR_UNSUPPORTED;
+  TW_TRY(device_check(nullptr));
+  tw::PtArgs a;
+  a.B = batch;
+  a.W = max_pages_per_seq;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.page_table = page_table;
+  a.keep = prefix_len / tw::kPage;
+  a.free_pages = free_pages;
+  a.cap = num_pool_pages;
+  a.num_free = num_free;
+  a.num_free_out = num_free_out;
+  a.out_lens = out_lens;
+  a.slots = slots;
+  a.num_slots = num_slots;
+  a.offsets = offsets;
+  const cudaError_t e = tw::launch_update_page_table(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+int tw_write_rows(const tw_kv* kv, const uint16_t* k_new, int64_t k_stride,
+                  const uint16_t* v_new, int64_t v_stride, const int32_t* slots,
+                  int32_t num_tokens, uint8_t* codes, uint16_t* scales, uint16_t* zeros,
+                  uint16_t* meta, void* stream) {
+  tw::Layout L;
+  TW_TRY(check_kv(kv, true, true, &L));
+  if (!codes != !scales || !codes != !zeros || num_tokens < 0) return TW_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(zeros, 16) || !aligned(meta, 16))
+    return TW_ERR_INVALID_ARG;
+  if (!k_new || !aligned(k_new, 16) || !v_new || !aligned(v_new, 16) || !slots ||
+      !aligned(slots, 4))
+    return TW_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)L.Hk * tw::kHeadDim;
+  if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return TW_ERR_INVALID_ARG;
+  const int64_t nslots =
+      L.page_table ? (int64_t)L.pool_pages * tw::kPage : (int64_t)L.B * L.N;
+  if (nslots > INT32_MAX) return TW_ERR_UNSUPPORTED;
+  if (num_tokens == 0 || nslots == 0) return TW_OK;
+  int sms = 0;
+  TW_TRY(device_check(&sms));
+  const cudaError_t e = tw::launch_write_rows(
+      L, reinterpret_cast<const __half*>(k_new), reinterpret_cast<const __half*>(v_new), k_stride,
+      v_stride, slots, num_tokens, reinterpret_cast<__half*>(const_cast<void*>(kv->k)),
+      reinterpret_cast<__half*>(const_cast<void*>(kv->v)), codes,
+      reinterpret_cast<__half*>(scales), reinterpret_cast<__half*>(zeros),
+      reinterpret_cast<__half*>(meta), static_cast<cudaStream_t>(stream), sms);
+  return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+int tw_prefix_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                             int32_t prefix_len, size_t* bytes) {
+  if (!bytes || batch < 0 || num_kv_heads < 1 || prefix_len < 0 || prefix_len % tw::kPage != 0)
+    return TW_ERR_INVALID_ARG;
+  TW_TRY(check_heads(num_q_heads, num_kv_heads));
+  *bytes = tw::prefix_decode_ws_bytes(batch, num_q_heads, num_kv_heads, prefix_len);
+  return TW_OK;
+}
+
+int tw_prefix_decode(const uint16_t* q, int32_t num_q_heads, const tw_kv* kv, int32_t prefix_len,
+                     uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  tw::Layout L;
+  TW_TRY(check_kv(kv, true, true, &L));
+  TW_TRY(check_heads(num_q_heads, L.Hk));
+  if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !aligned(lse, 4))
+    return TW_ERR_INVALID_ARG;
+  if (prefix_len < 0 || prefix_len % tw::kPage != 0 || prefix_len > L.N) return TW_ERR_INVALID_ARG;
+  // copies address the cache's rows by a signed 32-bit coordinate, the grids
+  // count sequences and heads in 32 bits
+  const int64_t nrows = L.page_table ? (int64_t)L.pool_pages * L.Hk * tw::kPage
+                                     : (int64_t)L.B * L.Hk * L.N;
+  if (nrows > INT32_MAX || (int64_t)L.B * num_q_heads > INT32_MAX / tw::kHeadDim)
+    return TW_ERR_UNSUPPORTED;
+  if (L.B == 0) return TW_OK;
+  TW_TRY(check_ws(ws, ws_bytes,
+                  tw::prefix_decode_ws_bytes(L.B, num_q_heads, L.Hk, prefix_len)));
+  TW_TRY(device_check(nullptr));
+  const cudaError_t e = tw::launch_prefix_decode(
+      L, reinterpret_cast<const __half*>(q), num_q_heads, prefix_len,
+      reinterpret_cast<const __half*>(kv->k), reinterpret_cast<const __half*>(kv->v),
+      reinterpret_cast<__half*>(out), lse, ws, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
 }  // extern "C"

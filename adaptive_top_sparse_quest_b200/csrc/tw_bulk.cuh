@@ -65,7 +65,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 
 // Wait until the phase of `bar` with the given parity has completed.  Gives
 // up after kWaitNs, setting kDevErrWait in *status (if given).
-__device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, int* status) {
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, int* status) {
   const unsigned long long t0 = global_ns();
   while (global_ns() - t0 < kWaitNs) {
 #pragma unroll 1

@@ -127,4 +127,37 @@ cudaError_t launch_resolve_rows(const Layout& L, int Hq, int group_sets, const i
                                 int icap, const int32_t* count, uint32_t* rows, cudaStream_t st,
                                 bool pdl);
 
+
+// Rows written by slot (cache_build.cu).
+constexpr int kWrMaxChunk = 16;
+cudaError_t launch_write_rows(const Layout& L, const __half* k_new, const __half* v_new,
+                              int64_t k_stride, int64_t v_stride, const int32_t* slots, int T,
+                              __half* K, __half* V, uint8_t* codes, __half* scales, __half* zeros,
+                              __half* meta, cudaStream_t st, int num_sms);
+
+// Page tables and slot maps from lengths (page_table.cu).
+constexpr int kPtMaxBatch = 8192;   // sequences: five words of shared memory each
+struct PtArgs {
+  int B, W;                    // sequences, page-table row length
+  const int32_t* seq_lens;     // [B] old lengths
+  const int32_t* new_lens;     // [B]
+  int32_t* page_table;         // [B][W]
+  int keep;                    // pages of the shared prefix at the head of every row
+  int32_t* free_pages;         // [cap] stack, cap = pages of the pool
+  int cap;
+  const int32_t* num_free;     // height before
+  int32_t* num_free_out;       // height after
+  int32_t* out_lens;           // [B] lengths reached
+  int32_t* slots;              // [num_slots] or null
+  int num_slots;
+  int32_t* offsets;            // [B + 1]
+};
+cudaError_t launch_update_page_table(const PtArgs& a, cudaStream_t st);
+
+// Dense attention of a batch behind a shared prefix (prefix_decode.cu).
+cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int prefix_len,
+                                 const __half* K, const __half* V, __half* out, float* lse,
+                                 void* ws, cudaStream_t st);
+size_t prefix_decode_ws_bytes(int B, int Hq, int Hk, int prefix_len);
+
 }  // namespace tw

@@ -359,6 +359,94 @@ const char* tw_decode_step_kernel_name(const tw_step* step, int32_t i);
 int tw_decode_step_profiled(const tw_step* step, void* const* events, int32_t n_events,
                             void* stream);
 
+/*
+ * Serving around the paged cache: page tables and slot maps from lengths, new
+ * K/V rows written by slot, and dense attention behind a shared prefix.  The
+ * pages on Twilight take a filled cache as given; these calls are this
+ * library's own way to fill one (its append step covers one token whose rows
+ * the caller has written) and the exact attention its pruning is compared
+ * with.  Use per serving step: tw_update_page_table once, then per layer
+ * tw_write_rows and tw_prefix_decode (or tw_decode_step on the same cache).
+ */
+
+/*
+ * Page tables and slot maps on the GPU, from the lengths of a batch before
+ * (seq_lens, clamped to [0, 16 W], W = max_pages_per_seq) and after
+ * (new_lens, below 0 read as 0) a serving step.  With
+ *   pages(n) = max(ceil(n / 16), prefix_len / 16):
+ *   - a sequence that shrinks gives its table entries pages(new) .. pages(old) - 1
+ *     back: they are pushed on the stack free_pages[0 .. *num_free), sequence
+ *     by sequence, lowest entry first (table entries are not cleared);
+ *   - then the sequences that grow take, in order, the pages they lack from
+ *     the stack's top and enter them in page_table; a growth is refused, and
+ *     the sequence keeps its length, pages and slots of -1, when new_lens
+ *     passes 16 W, when its tokens' places pass num_slots, or when the stack
+ *     does not hold its pages after those of all earlier growths (a growth
+ *     that needs no new page is then still served);
+ *   - out_lens[b] is the length reached, *num_free_out the stack's height;
+ *   - the new tokens are listed sequence by sequence: those of b at places
+ *     offsets[b] .. offsets[b + 1) (offsets: [B + 1], counting refused growths
+ *     too, at most 2^31 - 1), and slots[i] = 16 * page + position % 16 is the
+ *     cache slot of place i: -1 for a refused growth, for a position inside the
+ *     shared prefix and for places past the last token.
+ * The first prefix_len / 16 entries of every row belong to the caller (the
+ * pages of a prefix that the rows share): never taken, given or written.
+ * prefix_len is a multiple of 16, at most 16 W.  num_pool_pages is the stack's
+ * capacity; ids outside [0, num_pool_pages) in a table give slots of -1.
+ * slots may be NULL with num_slots 0 (a table only).  out_lens may be
+ * seq_lens or new_lens, num_free_out may be num_free (in place); no other
+ * arrays may overlap.  batch <= 8192, else TW_ERR_UNSUPPORTED; needs no
+ * workspace.  All arrays are int32 on the device, 4-byte aligned.
+ */
+int tw_update_page_table(int32_t batch, const int32_t* seq_lens, const int32_t* new_lens,
+                         int32_t* page_table, int32_t max_pages_per_seq, int32_t prefix_len,
+                         int32_t* free_pages, int32_t num_pool_pages, const int32_t* num_free,
+                         int32_t* num_free_out, int32_t* out_lens, int32_t* slots,
+                         int32_t num_slots, int32_t* offsets, void* stream);
+
+/*
+ * Write new rows into the cache by slot: row t of k_new / v_new (fp16, heads
+ * [Hk][128] side by side, k_stride / v_stride elements from a token to the
+ * next: multiples of 8, at least Hk * 128) goes to slot slots[t], 16 * pool
+ * page + row in a paged cache, b * max_seq_len + position in a contiguous one;
+ * a slot outside the cache (-1) skips the token.  In the same pass the key row
+ * is quantised into codes / scales / zeros exactly as tw_quantize_keys does
+ * (all NULL or all set) and folded into its page's meta (or NULL): a page
+ * whose row 0 is written starts anew, any other must be current for its
+ * earlier rows (bounds that are wider, as a page cut short leaves them, stay
+ * wider).  Rows of one page must stand in the list side by side on
+ * ascending slots, each slot once, as tw_update_page_table lists them; with
+ * codes and meta current before, the result then equals tw_quantize_keys and
+ * tw_page_meta for the new lengths bit for bit.  A page or slot that is
+ * listed in two places leaves that page's rows or metadata unspecified.
+ * kv->k and kv->v are written; kv->seq_lens and the entries of
+ * kv->page_table are not read (page_table only tells the layout).  k_new and
+ * v_new may not overlap the cache.  The cache's slots must number below 2^31.
+ */
+int tw_write_rows(const tw_kv* kv, const uint16_t* k_new, int64_t k_stride,
+                  const uint16_t* v_new, int64_t v_stride, const int32_t* slots,
+                  int32_t num_tokens, uint8_t* codes, uint16_t* scales, uint16_t* zeros,
+                  uint16_t* meta, void* stream);
+
+/*
+ * Dense decode attention of a batch whose sequences share their first
+ * prefix_len tokens, the shared rows read once for all sequences:
+ *   out[b][hq] = sum_{t < len_b} softmax_t(q . k_t / sqrt(128)) v_t
+ * (fp32 accumulation, fp16 result; lse [B][Hq] natural log, or NULL).  Tokens
+ * t < prefix_len are read from sequence 0's rows (its page_table entries 0 ..
+ * prefix_len / 16 - 1, or its contiguous rows, whatever seq_lens[0] says), the
+ * others from each sequence's own.  prefix_len is a multiple of 16 in
+ * [0, max_seq_len]; 0 shares nothing (plain dense decode).  A sequence shorter
+ * than the prefix attends to its first len_b tokens; an empty one gives out = 0
+ * and lse = -inf.  Rows at and past a sequence's end are not used, whatever
+ * they hold (NaN included).  Cache rows must number below 2^31.  Workspace:
+ * tw_prefix_workspace_size bytes.
+ */
+int tw_prefix_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                             int32_t prefix_len, size_t* bytes);
+int tw_prefix_decode(const uint16_t* q, int32_t num_q_heads, const tw_kv* kv, int32_t prefix_len,
+                     uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

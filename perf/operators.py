@@ -282,7 +282,7 @@ def _run_own(s):
     if op == "pages":
         u = s["update"]
         u(s["new"], s["num_free"])
-        return {"lens": u.seq_lens, "num_free": u.num_free, "table": s["table"],
+        return {"lens": u.seq_lens_out, "num_free": u.num_free_out, "table": s["table"],
                 "free": s["free"], "slots": u.slots, "offsets": u.offsets}
     s["tw"].write_rows(s["kv"], s["k_new"], s["v_new"], s["slots"], s["keys"], s["meta"])
     return {n: s[n] for n in ("k", "v", "codes", "scales", "zeros", "meta")}
