@@ -45,6 +45,38 @@ constexpr float kPdScale = 1.4426950408889634f * 0.08838834764831845f;   // log2
 constexpr float kLift = 7.f;                    // weights are 2^(s - m + 7), m within 2^8 of the maximum
 constexpr float kSlack = 8.f;
 
+// 2^x of two values by arithmetic, for some of the weights: the special-function
+// unit's 16 exponentials per clock and SM are what bounds the softmax (128 x 128
+// weights take it the 1024 clocks that the tile's two products take the tensor
+// cores).  x = n + f with n the nearest integer, f in [-1/2, 1/2] and 2^f by a
+// polynomial of degree 4 fitted to the least relative error, 2.6e-6: a 200th of
+// the rounding to fp16 that follows.  Below 2^-125 the result is 2^-125.
+__device__ __forceinline__ float2 ex2_poly(uint64_t x) {
+  const float2 v = f2_unpack(x);
+  x = f2_pack(fmaxf(v.x, -125.f), fmaxf(v.y, -125.f));
+  const uint64_t big = f2_pack(12582912.f, 12582912.f), neg = f2_pack(-12582912.f, -12582912.f);
+  const uint64_t t = f2_add(x, big);            // n in the low bits (1.5 * 2^23 + n)
+  const uint64_t n = f2_add(t, neg);
+  const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), x);
+  uint64_t p = f2_pack(0.00957010187736371f, 0.00957010187736371f);
+  p = f2_fma(p, f, f2_pack(0.05591786178285024f, 0.05591786178285024f));
+  p = f2_fma(p, f, f2_pack(0.24024744841456852f, 0.24024744841456852f));
+  p = f2_fma(p, f, f2_pack(0.6931218145593883f, 0.6931218145593883f));
+  p = f2_fma(p, f, f2_pack(0.9999992614376404f, 0.9999992614376404f));
+  const float2 pv = f2_unpack(p), tv = f2_unpack(t);
+  return make_float2(__uint_as_float(__float_as_uint(pv.x) + (__float_as_uint(tv.x) << 23)),
+                     __uint_as_float(__float_as_uint(pv.y) + (__float_as_uint(tv.y) << 23)));
+}
+
+// Maxima of 32 scores, four running ones.
+__device__ __forceinline__ void max32(const uint32_t* s, float* mx) {
+#pragma unroll
+  for (int z = 0; z < 32; z += 8)
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      mx[w] = max3(mx[w], __uint_as_float(s[z + 2 * w]), __uint_as_float(s[z + 2 * w + 1]));
+}
+
 struct PdRange {
   int p0, pm, p1, s0, sm, s1;   // prefix tiles [p0, pm, p1), own tiles [s0, sm, s1): stream 0 | 1
 };
@@ -419,62 +451,109 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         lim = min(lim, a.L.len(b));
       }
       float m = -INFINITY, l = 0.f;
+      // raise the running maximum (log2 units) to the tile's; past kSlack, or
+      // on the first tile, it is taken over and what is summed so far rescaled
+      auto raise = [&](const float* mx, bool first) {
+        const float top = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * kPdScale);
+        if (first) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, r < rows && top > m + kSlack)) {
+          // S is there, so the products before it are complete: O may be rescaled
+          const float f = top == -INFINITY ? 1.f : ex2(m - top);
+          l *= f;
+          m = top;
+#pragma unroll 1
+          for (int y = 0; y < 8; ++y) {
+            uint32_t o[16];
+            tmem_ld16(o_col + 16 * y, o);
+            tmem_wait_ld();
+            tmem_use16(o);
+#pragma unroll
+            for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+            tmem_st16(o_col + 16 * y, o);
+          }
+        }
+      };
+      // weights of 32 keys: fp16 into tensor memory, their sum to l
+      auto weights32 = [&](const uint32_t* s, int y, float lift) {
+        const uint64_t c2 = f2_pack(kPdScale, kPdScale), off2 = f2_pack(lift, lift);
+        uint64_t sum[2] = {0, 0};
+        uint32_t p[16];
+#pragma unroll
+        for (int z = 0; z < 16; ++z) {
+          const uint64_t e = f2_fma(f2_pack(__uint_as_float(s[2 * z]), __uint_as_float(s[2 * z + 1])),
+                                    c2, off2);
+          float2 w;
+          if (z % 4 == 3) {
+            w = ex2_poly(e);
+          } else {
+            w = f2_unpack(e);
+            w.x = ex2(w.x);
+            w.y = ex2(w.y);
+          }
+          sum[z & 1] = f2_add(sum[z & 1], f2_pack(w.x, w.y));
+          const __half2 hh = __floats2half2_rn(w.x, w.y);
+          p[z] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        tmem_st16(s_col + 16 * y, p);
+        const float2 t = f2_unpack(f2_add(sum[0], sum[1]));
+        l += t.x + t.y;
+      };
       for (int x = 0; x < g.n; ++x, ++nt) {
         ok = mbar_wait(&c.sfull[i], nt & 1, a.status);
         if (!ok) break;
         tc_fence_after();
         if (busy) {
-          uint32_t s[kTile];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) tmem_ld32(s_col + 32 * y, s + 32 * y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int y = 0; y < 4; ++y) tmem_use32(s + 32 * y);
-          const int ncol = lim - (g.t0 + x) * kTile;
-          if (!__all_sync(0xffffffffu, ncol >= kTile)) {
-#pragma unroll
-            for (int y = 0; y < kTile; ++y)
-              if (y >= ncol) s[y] = __float_as_uint(-INFINITY);
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int y = 0; y < kTile; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
-          const float top =
-              fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kPdScale);
-          if (x == 0) {
-            m = top;
-          } else if (__any_sync(0xffffffffu, r < rows && top > m + kSlack)) {
-            // S is there, so the products before it are complete: O may be rescaled
-            const float f = top == -INFINITY ? 1.f : ex2(m - top);
-            l *= f;
-            m = top;
+          const int ncol = lim - (g.t0 + x) * kTile;   // keys of the tile this row sees
+          if (__all_sync(0xffffffffu, ncol >= kTile)) {
+            // the scores are read twice, a chunk ahead of their use: holding a
+            // row of 128 would cost the registers that the exponentials need
+            uint32_t s[2][32];
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            tmem_ld32(s_col, s[0]);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              uint32_t o[32];
-              tmem_ld32(o_col + 32 * y, o);
               tmem_wait_ld();
-              tmem_use32(o);
+              tmem_use32(s[y & 1]);
+              tmem_ld32(s_col + 32 * ((y + 1) & 3), s[(y + 1) & 1]);
+              max32(s[y & 1], mx);
+            }
+            raise(mx, x == 0);
+            const float lift = kLift - m;
 #pragma unroll
-              for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
-              tmem_st32(o_col + 32 * y, o);
+            for (int y = 0; y < 4; ++y) {
+              tmem_wait_ld();
+              tmem_use32(s[y & 1]);
+              if (y < 3) tmem_ld32(s_col + 32 * (y + 1), s[(y + 1) & 1]);
+              weights32(s[y & 1], y, lift);   // over scores read already
+            }
+          } else {
+            // a tile that ends early, for some row at least: chunk by chunk,
+            // the scores read twice
+            const int nch = min(4, (g.keys - (g.t0 + x) * kTile + 31) / 32);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t s[32];
+            auto load = [&](int y) {
+              tmem_ld32(s_col + 32 * y, s);
+              tmem_wait_ld();
+              tmem_use32(s);
+#pragma unroll
+              for (int z = 0; z < 32; ++z)
+                if (32 * y + z >= ncol) s[z] = __float_as_uint(-INFINITY);
+            };
+#pragma unroll 1
+            for (int y = 0; y < nch; ++y) {
+              load(y);
+              max32(s, mx);
+            }
+            raise(mx, x == 0);
+            const float lift = m == -INFINITY ? 0.f : kLift - m;
+#pragma unroll 1
+            for (int y = 0; y < nch; ++y) {
+              load(y);
+              weights32(s, y, lift);   // over scores of chunks up to y / 2: read already
             }
           }
-          const float off = m == -INFINITY ? 0.f : kLift - m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            uint32_t p[16];
-#pragma unroll
-            for (int z = 0; z < 16; ++z) {
-              const float p0 = ex2(__fmaf_rn(__uint_as_float(s[32 * y + 2 * z]), kPdScale, off));
-              const float p1 = ex2(__fmaf_rn(__uint_as_float(s[32 * y + 2 * z + 1]), kPdScale, off));
-              sum[z & 3] += p0 + p1;
-              const __half2 hh = __floats2half2_rn(p0, p1);
-              p[z] = *reinterpret_cast<const uint32_t*>(&hh);
-            }
-            tmem_st16(s_col + 16 * y, p);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
         tc_fence_before();
