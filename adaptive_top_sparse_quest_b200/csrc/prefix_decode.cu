@@ -100,13 +100,17 @@ struct PdArgs {
 };
 
 struct PdCtl {
-  uint64_t kfull[2], vfull[2], kempty[2], vempty[2], qfull[2], sfull[2], pfull[2], ofull[2], drain;
+  uint64_t kfull[2], vfull[2], kempty[2], vempty[2], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], shared_done, drain;
   uint32_t tmem;
   int red[kPdThreads / 32];
   PdRange range;
   int at_b[2], at_h[2], at_t[2];   // where each stream's own tiles begin
 };
-constexpr size_t kPdSmem = 6 * kBuf + sizeof(PdCtl) + 1024;
+constexpr uint32_t kPdCtlBytes = 512;
+static_assert(sizeof(PdCtl) <= kPdCtlBytes, "control block");
+// Q, K, V tiles of both streams | control block | 4 KB per softmax warp to write
+// records through | alignment to 1 KB
+constexpr size_t kPdSmem = 6 * kBuf + kPdCtlBytes + 8 * 4096 + 1024;
 
 __device__ __forceinline__ int own_tiles(const PdArgs& a, int b) {
   const int n = a.L.len(b) - a.P;
@@ -175,6 +179,11 @@ struct SegIter {
   }
 };
 
+// First of the M = B * G query rows of a KV head that stream i holds (prefix).
+__device__ __forceinline__ int first_row(const PdArgs& a, const Seg& g, int i) {
+  return a.pair ? g.rt * 2 * kTile + i * kTile : 0;
+}
+
 // Query rows of a segment that stream i holds.
 __device__ __forceinline__ int seg_rows(const PdArgs& a, const Seg& g, int i) {
   if (!g.prefix) return a.G;
@@ -182,18 +191,13 @@ __device__ __forceinline__ int seg_rows(const PdArgs& a, const Seg& g, int i) {
   return left < 0 ? 0 : min(left, kTile);
 }
 
-// Which K / V buffers the k-th tile of a stream uses, and their how-manieth
-// fill that is.  Paired streams share the prefix tiles, which alternate
-// between the two buffer sets; other tiles use the stream's own.
-struct Fill {
-  int set, j;
-};
-__device__ __forceinline__ Fill fill_of(bool shared, int k, int i, int base) {
-  return shared ? Fill{k & 1, k >> 1} : Fill{i, base + k};
-}
+// A value that is the same in all lanes, in a form that lets the compiler know:
+// it then keeps operand descriptors in uniform registers.
+__device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __global__ void __launch_bounds__(kPdThreads, 1)
 k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_q1,
                 const __grid_constant__ PdArgs a) {
   extern __shared__ unsigned char pd_smem_raw[];
   const uint32_t raw = smem_u32(pd_smem_raw);
@@ -203,7 +207,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   auto k_buf = [&](int i) { return base + (2 + i) * kBuf; };
   auto v_buf = [&](int i) { return base + (4 + i) * kBuf; };
   PdCtl& c = *reinterpret_cast<PdCtl*>(smem + 6 * kBuf);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = (int)uni(tid >> 5);
   griddep_launch();   // the joining kernel waits for this grid's end by itself
 
   if (warp == 8) tmem_alloc(&c.tmem, 512);
@@ -213,68 +217,72 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       mbar_init(&c.vfull[i], 1);
       mbar_init(&c.kempty[i], 2);   // both streams, or one twice
       mbar_init(&c.vempty[i], 2);
-      mbar_init(&c.qfull[i], 4);
+      mbar_init(&c.qfull[i], 1);
+      mbar_init(&c.qempty[i], 1);
       mbar_init(&c.sfull[i], 1);
       mbar_init(&c.pfull[i], 4);
       mbar_init(&c.ofull[i], 1);
     }
+    mbar_init(&c.shared_done, 1);
     mbar_init(&c.drain, 2);
     mbar_fence_init();
   }
-  // own key tiles of all sequences, this CTA's share of all tiles
+  // own key tiles of all sequences, this CTA's share of all tiles, and where in
+  // the list of sequences its own tiles begin
   {
-    int sum = 0;
+    auto block_incl = [&](int v, int* all) {   // inclusive sum over the block
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+      }
+      if (lane == 31) c.red[warp] = v;
+      __syncthreads();
+      *all = 0;
+#pragma unroll
+      for (int w = 0; w < kPdThreads / 32; ++w) {
+        const int x = c.red[w];
+        if (w < warp) v += x;
+        *all += x;
+      }
+      return v;
+    };
+    int sum = 0, total;
     for (int b = tid; b < a.L.B; b += kPdThreads) sum += own_tiles(a, b);
-    sum = warp_sum(sum);
-    if (lane == 0) c.red[warp] = sum;
-    __syncthreads();
-    int total = 0;
-    for (int w = 0; w < kPdThreads / 32; ++w) total += c.red[w];
-    const int64_t S1 = (int64_t)a.L.Hk * a.RT * a.KT, S2 = (int64_t)total * a.L.Hk;
-    const int64_t X = S1 + S2;
+    const int incl0 = block_incl(sum, &total);
+    const int64_t S1 = (int64_t)a.L.Hk * a.RT * a.KT, X = S1 + (int64_t)total * a.L.Hk;
+    const int64_t x0 = X * blockIdx.x / kPdCtas, x1 = X * (blockIdx.x + 1) / kPdCtas;
+    PdRange r;
+    r.p0 = (int)min(x0, S1);
+    r.p1 = (int)min(x1, S1);
+    r.s0 = (int)(max(x0, S1) - S1);
+    r.s1 = (int)(max(x1, S1) - S1);
+    // an odd tile goes to stream 0, of both parts to one stream each
+    r.pm = r.p0 + (r.p1 - r.p0 + 1) / 2;
+    r.sm = r.s0 + (r.s1 - r.s0 + (!a.pair && ((r.p1 - r.p0) & 1) ? 0 : 1)) / 2;
     if (tid == 0) {
-      const int64_t x0 = X * blockIdx.x / gridDim.x, x1 = X * (blockIdx.x + 1) / gridDim.x;
-      PdRange r;
-      r.p0 = (int)min(x0, S1);
-      r.p1 = (int)min(x1, S1);
-      r.s0 = (int)(max(x0, S1) - S1);
-      r.s1 = (int)(max(x1, S1) - S1);
-      // an odd tile goes to stream 0, of both parts to one stream each
-      r.pm = r.p0 + (r.p1 - r.p0 + 1) / 2;
-      r.sm = r.s0 + (r.s1 - r.s0 + (!a.pair && ((r.p1 - r.p0) & 1) ? 0 : 1)) / 2;
       c.range = r;
       a.ranges[blockIdx.x] = r;
     }
-    __syncthreads();
-    // sequence, head and tile at which each stream's own tiles begin
     int before = 0;
     for (int b0 = 0; b0 < a.L.B; b0 += kPdThreads) {
       const int b = b0 + tid;
-      const int kt = b < a.L.B ? own_tiles(a, b) : 0;
-      int incl = kt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
+      int kt = sum, incl = incl0, chunk = total;
+      if (a.L.B > kPdThreads) {   // else the sums above are these
+        kt = b < a.L.B ? own_tiles(a, b) : 0;
+        __syncthreads();
+        incl = block_incl(kt, &chunk);
       }
-      __syncthreads();
-      if (lane == 31) c.red[warp] = incl;
-      __syncthreads();
-      int chunk = 0, wbefore = 0;
-      for (int w = 0; w < kPdThreads / 32; ++w) {
-        if (w < warp) wbefore += c.red[w];
-        chunk += c.red[w];
-      }
-      const int first = before + wbefore + incl - kt;
+      const int first = before + incl - kt;
       if (blockIdx.x == 0 && b < a.L.B) a.cum[b] = first;
       const int64_t lo = (int64_t)first * a.L.Hk;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t s = (i == 0 ? c.range.s0 : c.range.sm) - lo;
+        const int64_t s = (i == 0 ? r.s0 : r.sm) - lo;
         if (kt > 0 && s >= 0 && s < (int64_t)kt * a.L.Hk) {
           c.at_b[i] = b;
-          c.at_h[i] = (int)(s / kt);
-          c.at_t[i] = (int)(s % kt);
+          c.at_h[i] = (int)s / kt;
+          c.at_t[i] = (int)s % kt;
         }
       }
       before += chunk;
@@ -284,20 +292,34 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     __syncthreads();
     tc_fence_after();
   }
-  const uint32_t tmem = c.tmem;
+  const uint32_t tmem = uni(c.tmem);
   const int pairs = a.pair ? c.range.p1 - c.range.p0 : 0;   // tiles on shared buffers
 
   if (warp >= 10) {
-    // ---- producer of buffer set i: lane 2 j + half copies that half of page j's rows
+    // ---- producer of stream i's query rows and of buffer set i, which paired
+    // streams' shared tiles take in turn: lane 2 j + half copies that half of
+    // page j's rows
     const int i = warp - 10;
     SegIter it(a, c, i);
     Seg g;
     int k = 0;                                // tiles of this stream seen
     const int own0 = (pairs + 1 - i) / 2;     // shared fills of this set
     bool ok = true;
-    int kfills = 0, vfills = 0;
+    int kfills = 0, vfills = 0, nseg = 0;
     while (ok && it.next(a, i, g)) {
       const bool shared = a.pair && g.prefix;
+      if (seg_rows(a, g, i) > 0) {
+        // the segment's query rows: 128 of the M of its KV head, or a sequence's G
+        const int rows = g.prefix ? kTile : a.G;
+        const int b = g.prefix ? first_row(a, g, i) / a.G : g.b;
+        if (nseg > 0 && !mbar_wait(&c.qempty[i], (nseg - 1) & 1, a.status)) break;
+        if (lane == 0) mbar_arrive_tx(&c.qfull[i], rows * kHeadDim * 2);
+        __syncwarp();
+        if (lane < 2)
+          tma_load_3d(q_buf(i) + lane * kBlk, g.prefix ? &map_q : &map_q1, lane * 64, g.h * a.G, b,
+                      &c.qfull[i]);
+        ++nseg;
+      }
       for (int t = g.t0; t < g.t0 + g.n; ++t, ++k) {
         if (shared && (k & 1) != i) continue;
         const int j = shared ? k >> 1 : own0 + k - pairs;
@@ -318,62 +340,127 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         vfills = j + 1;
       }
     }
+    if (nseg > 0) mbar_wait(&c.qfull[i], (nseg - 1) & 1, a.status);
     // copies in flight land before the CTA may end (also after a wait gave up)
     if (kfills > 0) mbar_wait(&c.kfull[i], (kfills - 1) & 1, a.status);
     if (vfills > 0) mbar_wait(&c.vfull[i], (vfills - 1) & 1, a.status);
   } else if (warp >= 8) {
-    // ---- tensor-core issue of stream i
+    // ---- tensor-core issue.  Paired streams' shared tiles are issued by the
+    // first warp alone: what it issues runs in order, a stream's O += P V and
+    // next S as a block, while the other stream's softmax runs.  (Two warps'
+    // products take turns one by one, both streams' end late, and their softmax
+    // run, and wait, at the same time.)  Other tiles are bound by the copies:
+    // a warp per stream, so that neither waits for the other's.
     const int i = warp - 8;
-    const uint32_t s_col = tmem + i * kTile, o_col = tmem + 2 * kTile + i * kTile;
-    const uint64_t q_desc = umma_desc(q_buf(i), 16, 1024);
-    const int own0 = (pairs + 1 - i) / 2;
+    bool ok = true;
+    auto issue_s = [&](const int i, uint32_t set, uint32_t np) {   // S = Q K^T
+      const uint32_t s_col = tmem + i * kTile;
+      const uint64_t qd = umma_desc(q_buf(i), 16, 1024), kd = umma_desc(k_buf(set), 16, 1024);
+      const uint32_t id = umma_idesc(np * kPage, false);
+      umma_ss4(s_col, qd, kd, id, 0);
+      umma_ss4(s_col, qd + (kBlk >> 4), kd + (kBlk >> 4), id, 1);
+      umma_commit(&c.sfull[i]);
+    };
+    auto issue_o = [&](const int i, uint32_t set, uint32_t np, uint32_t more) {   // O += P V
+      const uint32_t s_col = tmem + i * kTile, o_col = tmem + 2 * kTile + i * kTile;
+      const uint64_t vd = umma_desc(v_buf(set), kBlk, 1024);
+      const uint32_t id = umma_idesc(kHeadDim, true);
+      if (np == kTilePages) {
+        umma_ts4(o_col, s_col, vd, id, more);
+        umma_ts4(o_col, s_col + 32, vd + 4 * (2048 >> 4), id, 1);
+      } else {
+        for (uint32_t y = 0; y < np; ++y)
+          umma_ts(o_col, s_col + y * 8, vd + y * (2048 >> 4), id, more | y);
+      }
+    };
     SegIter it(a, c, i);
     Seg g;
-    int k = 0, nt = 0, nseg = 0;   // tiles seen, tiles computed, segments computed
-    bool ok = true;
-    while (ok && it.next(a, i, g)) {
-      const bool shared = a.pair && g.prefix;
-      if (seg_rows(a, g, i) == 0) {
-        // no rows of this stream: only hand the shared buffers on
-        for (int x = 0; x < g.n && ok; ++x, ++k) {
-          const Fill f = fill_of(shared, shared ? k : k - pairs, i, own0);
-          ok = mbar_wait(&c.kfull[f.set], f.j & 1, a.status);
-          if (ok && lane == 0) mbar_arrive(&c.kempty[f.set]);
-          ok = ok && mbar_wait(&c.vfull[f.set], f.j & 1, a.status);
-          if (ok && lane == 0) mbar_arrive(&c.vempty[f.set]);
-          __syncwarp();
+    int nt = 0, nseg = 0;   // tiles and segments of this stream so far
+    if (a.pair) {
+      int k = 0, nt1 = 0, nseg1 = 0;
+      while (ok && it.p < it.pe && it.next(a, i, g)) {
+        const uint32_t two = uni(seg_rows(a, g, 1) > 0);   // the second stream has rows
+        if (i == 0) {
+          auto pages = [&](int x) {
+            return uni(min(kTilePages, (g.keys - (g.t0 + x) * kTile + kPage - 1) / kPage));
+          };
+          uint32_t set = uni(k & 1), np = pages(0);
+          ok = mbar_wait(&c.kfull[set], (k >> 1) & 1, a.status) &&
+               mbar_wait(&c.qfull[0], nseg & 1, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(0, set, np);
+          umma_commit(&c.kempty[set]);
+          if (two) {
+            ok = mbar_wait(&c.qfull[1], nseg1 & 1, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(1, set, np);
+          }
+          umma_commit(&c.kempty[set]);
+          for (int x = 0; x < g.n; ++x, ++k) {
+            const uint32_t last = uni(x == g.n - 1), more = uni(x > 0);
+            const uint32_t set_n = uni((k + 1) & 1), np_n = last ? 0 : pages(x + 1);
+            const int par_n = ((k + 1) >> 1) & 1;
+            ok = mbar_wait(&c.vfull[set], (k >> 1) & 1, a.status);
+            if (!ok) break;
+            for (int j = 0; j < 1 + (int)two; ++j) {
+              ok = mbar_wait(&c.pfull[j], (j ? nt1 + x : nt + x) & 1, a.status);
+              if (!ok) break;
+              tc_fence_after();
+              issue_o(j, set, np, more);
+              umma_commit(&c.vempty[set]);
+              if (!two) umma_commit(&c.vempty[set]);
+              if (last) {
+                umma_commit(&c.qempty[j]);
+                umma_commit(&c.ofull[j]);
+              } else {
+                if (j == 0) ok = mbar_wait(&c.kfull[set_n], par_n, a.status);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(j, set_n, np_n);
+                umma_commit(&c.kempty[set_n]);
+                if (!two) umma_commit(&c.kempty[set_n]);
+              }
+            }
+            if (!ok) break;
+            set = set_n;
+            np = np_n;
+          }
         }
-        continue;
+        nt += i == 0 || two ? g.n : 0;
+        nseg += i == 0 || two ? 1 : 0;
+        nt1 += two ? g.n : 0;
+        nseg1 += two ? 1 : 0;
       }
+      // the second warp goes on with its stream when its shared tiles are done
+      if (i == 0)
+        umma_commit(&c.shared_done);
+      else
+        ok = mbar_wait(&c.shared_done, 0, a.status);
+    }
+    int j = (pairs + 1 - i) / 2;   // fills of this stream's buffers so far
+    while (ok && it.next(a, i, g)) {
       ok = mbar_wait(&c.qfull[i], nseg & 1, a.status);
-      for (int x = 0; x < g.n && ok; ++x, ++k, ++nt) {
-        const Fill f = fill_of(shared, shared ? k : k - pairs, i, own0);
+      for (int x = 0; x < g.n && ok; ++x, ++j, ++nt) {
         const int valid = min(kTile, g.keys - (g.t0 + x) * kTile);
-        const int np = (valid + kPage - 1) / kPage;
-        ok = mbar_wait(&c.kfull[f.set], f.j & 1, a.status);
+        const uint32_t np = uni((valid + kPage - 1) / kPage);
+        const uint32_t last = uni(x == g.n - 1), more = uni(x > 0);
+        ok = mbar_wait(&c.kfull[i], j & 1, a.status);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t kd = umma_desc(k_buf(f.set), 16, 1024);
-          const uint32_t id = umma_idesc(np * kPage, false);
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            const uint32_t off = (s >> 2) * (kBlk >> 4) + (s & 3) * 2;
-            umma_ss(s_col, q_desc + off, kd + off, id, s > 0);
-          }
-          umma_commit(&c.sfull[i]);
-          umma_commit(&c.kempty[f.set]);
-          if (!shared) umma_commit(&c.kempty[f.set]);
-        }
-        __syncwarp();
-        ok = mbar_wait(&c.vfull[f.set], f.j & 1, a.status);
+        issue_s(i, i, np);
+        umma_commit(&c.kempty[i]);
+        umma_commit(&c.kempty[i]);
+        if (last) umma_commit(&c.qempty[i]);
+        ok = mbar_wait(&c.vfull[i], j & 1, a.status);
         if (!ok) break;
         if (valid & (kPage - 1)) {
           // rows past the sequence's end meet weights of zero, whatever they
           // hold: make them zero
-          const int nz = np * kPage - valid;
+          const int nz = (int)np * kPage - valid;
           for (int y = lane; y < nz * 16; y += 32) {
-            const uint32_t at = v_buf(f.set) + (y & 1) * kBlk + (valid + (y >> 4)) * 128 +
+            const uint32_t at = v_buf(i) + (y & 1) * kBlk + (valid + (y >> 4)) * 128 +
                                 ((y >> 1) & 7) * 16;
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
           }
@@ -383,21 +470,15 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         ok = mbar_wait(&c.pfull[i], nt & 1, a.status);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t vd = umma_desc(v_buf(f.set), kBlk, 1024);
-          const uint32_t id = umma_idesc(kHeadDim, true);
-          for (int s = 0; s < np; ++s)
-            umma_ts(o_col, s_col + s * 8, vd + s * (2048 >> 4), id, x > 0 || s > 0);
-          umma_commit(&c.vempty[f.set]);
-          if (!shared) umma_commit(&c.vempty[f.set]);
-          if (x == g.n - 1) umma_commit(&c.ofull[i]);
-        }
-        __syncwarp();
+        issue_o(i, i, np, more);
+        umma_commit(&c.vempty[i]);
+        umma_commit(&c.vempty[i]);
+        if (last) umma_commit(&c.ofull[i]);
       }
       ++nseg;
     }
     // this warp's products and their arrivals are done before the CTA may end
-    if (lane == 0) umma_commit(&c.drain);
+    umma_commit(&c.drain);
     mbar_wait(&c.drain, 0, a.status);
   } else {
     // ---- softmax of stream i, one query row per thread
@@ -406,50 +487,21 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + i * kTile, o_col = tmem + lanes + 2 * kTile + i * kTile;
     SegIter it(a, c, i);
-    Seg g, ng;
+    Seg g;
     int nt = 0, nseg = 0;
     bool ok = true;
-    // next segment with rows on this stream; its query rows into shared memory
+    // next segment with rows on this stream
     auto next = [&](Seg& s) {
       while (it.next(a, i, s))
         if (seg_rows(a, s, i) > 0) return true;
       return false;
     };
-    auto row_of = [&](const Seg& s, int& b, int& hq) {
-      const int m = s.prefix ? (a.pair ? s.rt * 2 * kTile + i * kTile : 0) + r : r;
-      b = s.prefix ? m / a.G : s.b;
-      hq = s.h * a.G + (s.prefix ? m % a.G : m);
-    };
-    auto load_q = [&](const Seg& s) {
-      if (r < seg_rows(a, s, i)) {
-        int b, hq;
-        row_of(s, b, hq);
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * a.Hq + hq) * kHeadDim);
-        const uint32_t dst = q_buf(i) + r * 128;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const uint4 v = __ldg(src + x);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           dst + (x >> 3) * kBlk + (((x & 7) ^ (r & 7)) * 16)),
-                       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                       : "memory");
-        }
-      }
-      fence_async_proxy();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.qfull[i]);
-    };
     bool have = next(g);
-    if (have) load_q(g);
     while (have && ok) {
       const int rows = seg_rows(a, g, i);
       const bool busy = (warp & 3) * 32 < rows;   // this warp has rows
       int lim = g.keys;                            // keys this row sees
-      if (g.prefix && r < rows) {
-        int b, hq;
-        row_of(g, b, hq);
-        lim = min(lim, a.L.len(b));
-      }
+      if (g.prefix && r < rows) lim = min(lim, a.L.len((first_row(a, g, i) + r) / a.G));
       float m = -INFINITY, l = 0.f;
       // raise the running maximum (log2 units) to the tile's; past kSlack, or
       // on the first tile, it is taken over and what is summed so far rescaled
@@ -561,32 +613,45 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         if (lane == 0) mbar_arrive(&c.pfull[i]);
       }
       if (!ok) break;
-      // the next segment's query rows go in while this one's last product runs
-      have = next(ng);
-      if (have) load_q(ng);
       ok = mbar_wait(&c.ofull[i], nseg & 1, a.status);
       if (!ok) break;
       ++nseg;
       tc_fence_after();
       if (busy) {
         const int per = g.prefix ? a.rows1 : a.G;
-        const int64_t at = g.slot * per + (g.prefix && a.pair ? i * kTile : 0) + r;
+        const int64_t at = g.slot * per + (g.prefix && a.pair ? i * kTile : 0);
+        if (r < rows) (g.prefix ? a.ml1 : a.ml2)[at + r] = make_float2(m - kLift, l);
+        // 32 columns of the warp's rows at a time, through shared memory, so that
+        // eight lanes write 128 bytes of one row
         float* o_dst = (g.prefix ? a.o1 : a.o2) + at * kHeadDim;
-        if (r < rows) (g.prefix ? a.ml1 : a.ml2)[at] = make_float2(m - kLift, l);
-#pragma unroll
+        const uint32_t stage = base + 6 * kBuf + kPdCtlBytes + warp * 4096;
+#pragma unroll 1
         for (int y = 0; y < 4; ++y) {
           uint32_t o[32];
           tmem_ld32(o_col + 32 * y, o);
           tmem_wait_ld();
           tmem_use32(o);
-          if (r < rows)
 #pragma unroll
-            for (int z = 0; z < 8; ++z)
-              reinterpret_cast<uint4*>(o_dst + 32 * y)[z] =
-                  make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+          for (int z = 0; z < 8; ++z)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             stage + lane * 128 + ((z ^ (lane & 7)) * 16)),
+                         "r"(o[4 * z]), "r"(o[4 * z + 1]), "r"(o[4 * z + 2]), "r"(o[4 * z + 3])
+                         : "memory");
+          __syncwarp();
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            const int w = 4 * z + (lane >> 3), rr = (warp & 3) * 32 + w;
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(stage + w * 128 + (((lane & 7) ^ (w & 7)) * 16)));
+            if (rr < rows)
+              *reinterpret_cast<uint4*>(o_dst + (int64_t)rr * kHeadDim + 32 * y + 4 * (lane & 7)) = v;
+          }
+          __syncwarp();
         }
       }
-      g = ng;
+      have = next(g);
     }
   }
   tc_fence_before();
@@ -595,96 +660,108 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   if (warp == 8) tmem_free(tmem, 512);
 }
 
-// Join a row's records: a warp per output row, four channels per lane.
+// Join a row's records: a block per output row.  A thread looks up each record
+// that may be there; every warp forms the weights, takes every fourth record
+// with four channels per lane, four loads in flight, and the warps' sums are
+// added in order, so that the result does not depend on timing.
 constexpr int kJoinThreads = 128;
+constexpr int kJoinMax = 4 * kPdCtas;   // records of a row at most: two per CTA and part
 
 __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_constant__ PdArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t bh = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  griddep_wait();
-  if (bh >= (int64_t)a.L.B * a.Hq) return;
+  __shared__ float2 ml_s[kJoinMax];
+  __shared__ const float4* o_s[kJoinMax];
+  __shared__ float4 acc_s[kJoinThreads / 32][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t bh = blockIdx.x;
   const int b = (int)(bh / a.Hq), hq = (int)(bh % a.Hq), h = hq / a.G, g = hq % a.G;
+  griddep_wait();
   const int64_t S1 = (int64_t)a.L.Hk * a.RT * a.KT;
-  const int64_t X = S1 + (int64_t)__ldcg(a.cum + a.L.B) * a.L.Hk;
-  float M = -INFINITY, Ls = 0.f;
-  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-  // records of tiles [first, first + n) of the prefix's (part 0) or the own
-  // (part 1) list, written to slot worker + u, row `row`
+  const int len = a.L.len(b), total = __ldcg(a.cum + a.L.B), c0 = __ldcg(a.cum + b),
+            n2 = __ldcg(a.cum + b + 1) - c0;
+  const int64_t X = S1 + (int64_t)total * a.L.Hk;
+  // tile x of all X lies with CTA floor(x kPdCtas / X) or, after rounding, a
+  // neighbour; the CTAs' own ranges decide
+  const float per_tile = (float)kPdCtas / (float)max(X, (int64_t)1);
+  int cnt = 0;
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
-    int64_t first, u;
-    int n, per, row;
-    if (part == 0) {
-      const int m = b * a.G + g;
-      u = (int64_t)h * a.RT + (a.pair ? m / (2 * kTile) : 0);
-      first = u * a.KT;
-      n = a.L.len(b) > 0 ? a.KT : 0;
-      per = a.rows1;
-      row = a.pair ? m % (2 * kTile) : m;
-    } else {
-      const int c0 = __ldcg(a.cum + b);
-      n = __ldcg(a.cum + b + 1) - c0;
-      u = (int64_t)b * a.L.Hk + h;
-      first = (int64_t)c0 * a.L.Hk + (int64_t)h * n;
-      per = a.G;
-      row = g;
-    }
+    // records of tiles [first, first + n) of the prefix's (part 0) or the own
+    // (part 1) list, written to slot worker + u, row `row` of `per`
+    const int n = part ? n2 : len > 0 ? a.KT : 0;
     if (n == 0) continue;
+    const int m = b * a.G + g;
+    const int64_t u = part ? (int64_t)b * a.L.Hk + h
+                           : (int64_t)h * a.RT + (a.pair ? m / (2 * kTile) : 0);
+    const int64_t first = part ? (int64_t)c0 * a.L.Hk + (int64_t)h * n : u * a.KT;
+    const int per = part ? a.G : a.rows1, row = part ? g : a.pair ? m % (2 * kTile) : m;
     const int split = part == 0 && a.pair ? 1 : 2;   // records per CTA at most
-    // tile x of all X lies with CTA c when X c / n_ctas <= x
-    const int64_t x0 = first + (part ? S1 : 0), x1 = x0 + n - 1;
-    const int c_lo = (int)(((x0 + 1) * kPdCtas + X - 1) / X - 1);
-    const int c_hi = (int)(((x1 + 1) * kPdCtas + X - 1) / X - 1);
+    const int64_t x0 = first + (part ? S1 : 0);
+    const int c_lo = max(0, (int)((float)x0 * per_tile) - 1);
+    const int c_hi = min(kPdCtas - 1, (int)((float)(x0 + n) * per_tile) + 1);
     const int nw = (c_hi - c_lo + 1) * split;
-    const float2* ml = part ? a.ml2 : a.ml1;
-    const float* o = part ? a.o2 : a.o1;
-    for (int w0 = 0; w0 < nw; w0 += 32) {
-      const int w = w0 + lane, cta = c_lo + w / split;
-      float2 v = make_float2(-INFINITY, 0.f);
-      int64_t at = 0;
-      if (w < nw) {
-        const PdRange rg = a.ranges[cta];
-        int lo = part ? rg.s0 : rg.p0, hi = part ? rg.s1 : rg.p1;
-        if (split == 2) {
-          const int mid = part ? rg.sm : rg.pm;
-          if (w % 2 == 0) hi = mid; else lo = mid;
-        }
-        if (max((int64_t)lo, first) < min((int64_t)hi, first + n)) {
-          const int64_t slot = (split == 2 ? 2 * cta + w % 2 : cta) + u;
-          at = slot * per + row;
-          v = __ldcg(ml + at);
-        }
+    for (int w = tid; w < nw; w += kJoinThreads) {
+      const int cta = c_lo + w / split, i = w % split;
+      const PdRange rg = a.ranges[cta];
+      int lo = part ? rg.s0 : rg.p0, hi = part ? rg.s1 : rg.p1;
+      if (split == 2) {
+        const int mid = part ? rg.sm : rg.pm;
+        if (i == 0) hi = mid; else lo = mid;
       }
-      const float top = fmaxf(M, warp_max(v.x));
-      if (top == -INFINITY) continue;
-      const float keep = M == -INFINITY ? 0.f : ex2(M - top);
-      const float f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
-      M = top;
-      Ls = Ls * keep + warp_sum(v.y * f);
-      A.x *= keep;
-      A.y *= keep;
-      A.z *= keep;
-      A.w *= keep;
-      unsigned todo = __ballot_sync(0xffffffffu, f != 0.f);
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const float fs = __shfl_sync(0xffffffffu, f, src);
-        const int64_t as = __shfl_sync(0xffffffffu, at, src);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(o + as * kHeadDim) + lane);
-        A.x = __fmaf_rn(fs, x.x, A.x);
-        A.y = __fmaf_rn(fs, x.y, A.y);
-        A.z = __fmaf_rn(fs, x.z, A.z);
-        A.w = __fmaf_rn(fs, x.w, A.w);
+      const int64_t at = ((int64_t)split * cta + i + u) * per + row;
+      float2 v = make_float2(-INFINITY, 0.f);
+      if (max((int64_t)lo, first) < min((int64_t)hi, first + n))
+        v = __ldcg((part ? a.ml2 : a.ml1) + at);
+      ml_s[cnt + w] = v;
+      o_s[cnt + w] = reinterpret_cast<const float4*>((part ? a.o2 : a.o1) + at * kHeadDim);
+    }
+    cnt += nw;
+  }
+  __syncthreads();
+  float M = -INFINITY;
+  for (int k = lane; k < cnt; k += 32) M = fmaxf(M, ml_s[k].x);
+  M = warp_max(M);
+  float Ls = 0.f;
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M != -INFINITY) {
+    for (int k = lane; k < cnt; k += 32) Ls += ml_s[k].y * ex2(ml_s[k].x - M);
+    Ls = warp_sum(Ls);
+    for (int k0 = warp; k0 < cnt; k0 += 4 * (kJoinThreads / 32)) {
+      float4 x[4];
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * (kJoinThreads / 32);
+        f[j] = k < cnt ? ex2(ml_s[k].x - M) : 0.f;   // 0 where there is no record
+        x[j] = f[j] != 0.f ? __ldcg(o_s[k] + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        A.x = __fmaf_rn(f[j], x[j].x, A.x);
+        A.y = __fmaf_rn(f[j], x[j].y, A.y);
+        A.z = __fmaf_rn(f[j], x[j].z, A.z);
+        A.w = __fmaf_rn(f[j], x[j].w, A.w);
       }
     }
   }
-  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-  const __half2 o2[2] = {__floats2half2_rn(A.x * inv, A.y * inv),
-                         __floats2half2_rn(A.z * inv, A.w * inv)};
-  *reinterpret_cast<uint2*>(a.out + bh * kHeadDim + 4 * lane) = *reinterpret_cast<const uint2*>(o2);
-  if (a.lse && lane == 0)
-    a.lse[bh] = Ls > 0.f ? (M + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+  acc_s[warp][lane] = A;
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int w = 1; w < kJoinThreads / 32; ++w) {
+      const float4 e = acc_s[w][lane];
+      A.x += e.x;
+      A.y += e.y;
+      A.z += e.z;
+      A.w += e.w;
+    }
+    const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+    const __half2 o2[2] = {__floats2half2_rn(A.x * inv, A.y * inv),
+                           __floats2half2_rn(A.z * inv, A.w * inv)};
+    *reinterpret_cast<uint2*>(a.out + bh * kHeadDim + 4 * lane) =
+        *reinterpret_cast<const uint2*>(o2);
+    if (a.lse && lane == 0)
+      a.lse[bh] = Ls > 0.f ? (M + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+  }
 }
 
 // Workspace: status word | CTA ranges | own tiles before each sequence |
@@ -732,7 +809,8 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-static cudaError_t encode_rows(CUtensorMap* map, const __half* p, int64_t rows) {
+static cudaError_t encode(CUtensorMap* map, const __half* p, int rank, const cuuint64_t* dims,
+                          const cuuint64_t* strides, const cuuint32_t* box) {
   static std::atomic<void*> fn{nullptr};
   void* f = fn.load(std::memory_order_acquire);
   if (!f) {
@@ -743,13 +821,28 @@ static cudaError_t encode_rows(CUtensorMap* map, const __half* p, int64_t rows) 
     if (res != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
     fn.store(f, std::memory_order_release);
   }
-  const cuuint64_t dims[2] = {kHeadDim, (cuuint64_t)rows}, strides[1] = {kHeadDim * 2};
-  const cuuint32_t box[2] = {64, kPage}, step[2] = {1, 1};
+  const cuuint32_t step[3] = {1, 1, 1};
   const CUresult r = reinterpret_cast<EncodeTiled>(f)(
-      map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half*>(p), dims, strides, box, step,
+      map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<__half*>(p), dims, strides, box, step,
       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// K or V as rows of 128: boxes of 16 rows (a page) by 64 columns.
+static cudaError_t encode_rows(CUtensorMap* map, const __half* p, int64_t rows) {
+  const cuuint64_t dims[2] = {kHeadDim, (cuuint64_t)rows}, strides[1] = {kHeadDim * 2};
+  const cuuint32_t box[2] = {64, kPage};
+  return encode(map, p, 2, dims, strides, box);
+}
+
+// q [B][Hq][128]: boxes of a KV head's G query heads of `seqs` sequences by 64
+// columns; sequences past the batch are filled with zeros.
+static cudaError_t encode_q(CUtensorMap* map, const __half* q, int B, int Hq, int G, int seqs) {
+  const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)Hq, (cuuint64_t)B};
+  const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)Hq * kHeadDim * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)seqs};
+  return encode(map, q, 3, dims, strides, box);
 }
 
 cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int prefix_len,
@@ -782,24 +875,24 @@ cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int p
                                     : (int64_t)L.B * L.Hk * L.N;
   cudaError_t e;
   if (rows > 0) {   // a cache without rows has no tiles: no copy uses the maps
-    CUtensorMap mk, mv;
+    CUtensorMap mk, mv, mq, mq1;
     if ((e = encode_rows(&mk, K, rows)) != cudaSuccess) return e;
     if ((e = encode_rows(&mv, V, rows)) != cudaSuccess) return e;
+    if ((e = encode_q(&mq, q, L.B, Hq, a.G, kTile / a.G)) != cudaSuccess) return e;
+    if ((e = encode_q(&mq1, q, L.B, Hq, a.G, 1)) != cudaSuccess) return e;
     static std::atomic<int> done[kMaxDevices];
     e = once_per_device(done, [] {
       return cudaFuncSetAttribute(k_prefix_decode, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)kPdSmem);
     });
     if (e != cudaSuccess) return e;
-    e = launch_k(k_prefix_decode, dim3(kPdCtas), dim3(kPdThreads), kPdSmem, st, false, mk, mv, a);
+    e = launch_k(k_prefix_decode, dim3(kPdCtas), dim3(kPdThreads), kPdSmem, st, false, mk, mv, mq, mq1,
+                 a);
     if (e != cudaSuccess) return e;
   } else if ((e = cudaMemsetAsync(a.cum, 0, ((size_t)L.B + 1) * sizeof(int), st)) != cudaSuccess) {
     return e;
   }
-  const int64_t out_rows = (int64_t)L.B * Hq;
-  constexpr int per = kJoinThreads / 32;
-  return launch_k(k_prefix_join, dim3((unsigned)((out_rows + per - 1) / per)), dim3(kJoinThreads),
-                  0, st, rows > 0, a);
+  return launch_k(k_prefix_join, dim3((unsigned)(L.B * Hq)), dim3(kJoinThreads), 0, st, rows > 0, a);
 }
 
 }  // namespace tw
