@@ -623,7 +623,8 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         if (r < rows) (g.prefix ? a.ml1 : a.ml2)[at + r] = make_float2(m - kLift, l);
         // 32 columns of the warp's rows at a time, through shared memory, so that
         // eight lanes write 128 bytes of one row
-        float* o_dst = (g.prefix ? a.o1 : a.o2) + at * kHeadDim;
+        const int row0 = (warp & 3) * 32, nrow = min(32, rows - row0);
+        float* o_dst = (g.prefix ? a.o1 : a.o2) + (at + row0) * kHeadDim;
         const uint32_t stage = base + 6 * kBuf + kPdCtlBytes + warp * 4096;
 #pragma unroll 1
         for (int y = 0; y < 4; ++y) {
@@ -638,15 +639,14 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
                          "r"(o[4 * z]), "r"(o[4 * z + 1]), "r"(o[4 * z + 2]), "r"(o[4 * z + 3])
                          : "memory");
           __syncwarp();
-#pragma unroll
-          for (int z = 0; z < 8; ++z) {
-            const int w = 4 * z + (lane >> 3), rr = (warp & 3) * 32 + w;
+          for (int z = 0; z < (nrow + 3) / 4; ++z) {
+            const int w = 4 * z + (lane >> 3);
             uint4 v;
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                          : "r"(stage + w * 128 + (((lane & 7) ^ (w & 7)) * 16)));
-            if (rr < rows)
-              *reinterpret_cast<uint4*>(o_dst + (int64_t)rr * kHeadDim + 32 * y + 4 * (lane & 7)) = v;
+            if (w < nrow)
+              *reinterpret_cast<uint4*>(o_dst + w * kHeadDim + 32 * y + 4 * (lane & 7)) = v;
           }
           __syncwarp();
         }
@@ -660,21 +660,24 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   if (warp == 8) tmem_free(tmem, 512);
 }
 
-// Join a row's records: a block per output row.  A thread looks up each record
-// that may be there; every warp forms the weights, takes every fourth record
-// with four channels per lane, four loads in flight, and the warps' sums are
-// added in order, so that the result does not depend on timing.
+// Join a row's records: W warps per output row.  A warp's lanes look 32 records
+// up at a time, of those that may be there; the warp then adds them with four
+// channels per lane, four loads in flight; the warps' sums are added in order,
+// so that the result does not depend on timing.  W = 4 where the prefix's
+// records are many (few units, split over many CTAs), else 1.
 constexpr int kJoinThreads = 128;
-constexpr int kJoinMax = 4 * kPdCtas;   // records of a row at most: two per CTA and part
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinMany = 12;
 
+template <int W>
 __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_constant__ PdArgs a) {
-  __shared__ float2 ml_s[kJoinMax];
-  __shared__ const float4* o_s[kJoinMax];
-  __shared__ float4 acc_s[kJoinThreads / 32][32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t bh = blockIdx.x;
-  const int b = (int)(bh / a.Hq), hq = (int)(bh % a.Hq), h = hq / a.G, g = hq % a.G;
+  __shared__ float4 acc_s[kJoinWarps][32];
+  __shared__ float2 ml_s[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W;
+  const int64_t bh = (int64_t)blockIdx.x * (kJoinWarps / W) + (threadIdx.x >> 5) / W;
   griddep_wait();
+  if (W < kJoinWarps && bh >= (int64_t)a.L.B * a.Hq) return;
+  const int b = (int)(bh / a.Hq), hq = (int)(bh % a.Hq), h = hq / a.G, g = hq % a.G;
   const int64_t S1 = (int64_t)a.L.Hk * a.RT * a.KT;
   const int len = a.L.len(b), total = __ldcg(a.cum + a.L.B), c0 = __ldcg(a.cum + b),
             n2 = __ldcg(a.cum + b + 1) - c0;
@@ -682,7 +685,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
   // tile x of all X lies with CTA floor(x kPdCtas / X) or, after rounding, a
   // neighbour; the CTAs' own ranges decide
   const float per_tile = (float)kPdCtas / (float)max(X, (int64_t)1);
-  int cnt = 0;
+  float M = -INFINITY, Ls = 0.f;
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
     // records of tiles [first, first + n) of the prefix's (part 0) or the own
@@ -699,69 +703,82 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
     const int c_lo = max(0, (int)((float)x0 * per_tile) - 1);
     const int c_hi = min(kPdCtas - 1, (int)((float)(x0 + n) * per_tile) + 1);
     const int nw = (c_hi - c_lo + 1) * split;
-    for (int w = tid; w < nw; w += kJoinThreads) {
-      const int cta = c_lo + w / split, i = w % split;
-      const PdRange rg = a.ranges[cta];
-      int lo = part ? rg.s0 : rg.p0, hi = part ? rg.s1 : rg.p1;
-      if (split == 2) {
-        const int mid = part ? rg.sm : rg.pm;
-        if (i == 0) hi = mid; else lo = mid;
-      }
-      const int64_t at = ((int64_t)split * cta + i + u) * per + row;
+    const float2* ml = part ? a.ml2 : a.ml1;
+    const float4* o = reinterpret_cast<const float4*>(part ? a.o2 : a.o1);
+    for (int w0 = warp; w0 < nw; w0 += 32 * W) {
+      const int w = w0 + lane * W, cta = c_lo + w / split, i = w % split;
       float2 v = make_float2(-INFINITY, 0.f);
-      if (max((int64_t)lo, first) < min((int64_t)hi, first + n))
-        v = __ldcg((part ? a.ml2 : a.ml1) + at);
-      ml_s[cnt + w] = v;
-      o_s[cnt + w] = reinterpret_cast<const float4*>((part ? a.o2 : a.o1) + at * kHeadDim);
-    }
-    cnt += nw;
-  }
-  __syncthreads();
-  float M = -INFINITY;
-  for (int k = lane; k < cnt; k += 32) M = fmaxf(M, ml_s[k].x);
-  M = warp_max(M);
-  float Ls = 0.f;
-  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M != -INFINITY) {
-    for (int k = lane; k < cnt; k += 32) Ls += ml_s[k].y * ex2(ml_s[k].x - M);
-    Ls = warp_sum(Ls);
-    for (int k0 = warp; k0 < cnt; k0 += 4 * (kJoinThreads / 32)) {
-      float4 x[4];
-      float f[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + j * (kJoinThreads / 32);
-        f[j] = k < cnt ? ex2(ml_s[k].x - M) : 0.f;   // 0 where there is no record
-        x[j] = f[j] != 0.f ? __ldcg(o_s[k] + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+      int64_t at = 0;
+      if (w < nw) {
+        const PdRange rg = a.ranges[cta];
+        int lo = part ? rg.s0 : rg.p0, hi = part ? rg.s1 : rg.p1;
+        if (split == 2) {
+          const int mid = part ? rg.sm : rg.pm;
+          if (i == 0) hi = mid; else lo = mid;
+        }
+        at = ((int64_t)split * cta + i + u) * per + row;
+        if (max((int64_t)lo, first) < min((int64_t)hi, first + n)) v = __ldcg(ml + at);
       }
+      const float top = fmaxf(M, warp_max(v.x));
+      if (top == -INFINITY) continue;
+      const float keep = M == -INFINITY ? 0.f : ex2(M - top);
+      const float f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
+      M = top;
+      Ls = Ls * keep + warp_sum(v.y * f);
+      A.x *= keep;
+      A.y *= keep;
+      A.z *= keep;
+      A.w *= keep;
+      unsigned todo = __ballot_sync(0xffffffffu, f != 0.f);
+      while (todo) {
+        float4 x[4];
+        float fs[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        A.x = __fmaf_rn(f[j], x[j].x, A.x);
-        A.y = __fmaf_rn(f[j], x[j].y, A.y);
-        A.z = __fmaf_rn(f[j], x[j].z, A.z);
-        A.w = __fmaf_rn(f[j], x[j].w, A.w);
+        for (int j = 0; j < 4; ++j) {
+          const int src = todo ? __ffs(todo) - 1 : 0;
+          fs[j] = __shfl_sync(0xffffffffu, f, src);
+          const int64_t as = __shfl_sync(0xffffffffu, at, src);
+          if (!todo) fs[j] = 0.f;
+          x[j] = todo ? __ldcg(o + as * (kHeadDim / 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+          todo &= todo - 1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          A.x = __fmaf_rn(fs[j], x[j].x, A.x);
+          A.y = __fmaf_rn(fs[j], x[j].y, A.y);
+          A.z = __fmaf_rn(fs[j], x[j].z, A.z);
+          A.w = __fmaf_rn(fs[j], x[j].w, A.w);
+        }
       }
     }
   }
-  acc_s[warp][lane] = A;
-  __syncthreads();
-  if (warp == 0) {
+  if (W > 1) {
+    acc_s[warp][lane] = A;
+    if (lane == 0) ml_s[warp] = make_float2(M, Ls);
+    __syncthreads();
+    if (warp != 0) return;
 #pragma unroll
-    for (int w = 1; w < kJoinThreads / 32; ++w) {
+    for (int w = 1; w < W; ++w) M = fmaxf(M, ml_s[w].x);
+    Ls = 0.f;
+    A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 v = ml_s[w];
+      const float f = v.x == -INFINITY ? 0.f : ex2(v.x - M);
       const float4 e = acc_s[w][lane];
-      A.x += e.x;
-      A.y += e.y;
-      A.z += e.z;
-      A.w += e.w;
+      Ls = __fmaf_rn(v.y, f, Ls);
+      A.x = __fmaf_rn(e.x, f, A.x);
+      A.y = __fmaf_rn(e.y, f, A.y);
+      A.z = __fmaf_rn(e.z, f, A.z);
+      A.w = __fmaf_rn(e.w, f, A.w);
     }
-    const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-    const __half2 o2[2] = {__floats2half2_rn(A.x * inv, A.y * inv),
-                           __floats2half2_rn(A.z * inv, A.w * inv)};
-    *reinterpret_cast<uint2*>(a.out + bh * kHeadDim + 4 * lane) =
-        *reinterpret_cast<const uint2*>(o2);
-    if (a.lse && lane == 0)
-      a.lse[bh] = Ls > 0.f ? (M + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
   }
+  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+  const __half2 o2[2] = {__floats2half2_rn(A.x * inv, A.y * inv),
+                         __floats2half2_rn(A.z * inv, A.w * inv)};
+  *reinterpret_cast<uint2*>(a.out + bh * kHeadDim + 4 * lane) = *reinterpret_cast<const uint2*>(o2);
+  if (a.lse && lane == 0)
+    a.lse[bh] = Ls > 0.f ? (M + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Workspace: status word | CTA ranges | own tiles before each sequence |
@@ -892,7 +909,15 @@ cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int p
   } else if ((e = cudaMemsetAsync(a.cum, 0, ((size_t)L.B + 1) * sizeof(int), st)) != cudaSuccess) {
     return e;
   }
-  return launch_k(k_prefix_join, dim3((unsigned)(L.B * Hq)), dim3(kJoinThreads), 0, st, rows > 0, a);
+  // records of a row of the prefix: the CTAs that share its unit, two streams each
+  const int64_t S1 = (int64_t)L.Hk * a.RT * a.KT;
+  const int64_t many = S1 > 0 ? (int64_t)a.KT * kPdCtas / S1 * (a.pair ? 1 : 2) : 0;
+  const int64_t out_rows = (int64_t)L.B * Hq;
+  if (many >= kJoinMany)
+    return launch_k(k_prefix_join<kJoinWarps>, dim3((unsigned)out_rows), dim3(kJoinThreads), 0, st,
+                    rows > 0, a);
+  return launch_k(k_prefix_join<1>, dim3((unsigned)((out_rows + kJoinWarps - 1) / kJoinWarps)),
+                  dim3(kJoinThreads), 0, st, rows > 0, a);
 }
 
 }  // namespace tw
