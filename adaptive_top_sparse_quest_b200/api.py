@@ -103,20 +103,11 @@ class KVCache:
         return (self.N + PAGE - 1) // PAGE
 
     def struct(self) -> TwKv:
-        s = TwKv()
-        s.k = _ptr(self.k)
-        s.v = _ptr(self.v)
-        s.batch = self.B
-        s.num_kv_heads = self.Hk
-        s.max_seq_len = self.N
-        s.seq_lens = _ptr(self.seq_lens)
-        s.page_table = _ptr(self.page_table)
-        s.max_pages_per_seq = int(self.page_table.shape[1]) if self.paged else 0
-        s.num_pool_pages = int(self.k.shape[0]) if self.paged else 0
-        s.page_size = PAGE
-        s.head_dim = HEAD_DIM
-        s.key_bits = self.key_bits
-        return s
+        paged = self.paged
+        N = self.N
+        return TwKv(_ptr(self.k), _ptr(self.v), self.B, self.Hk, N, _ptr(self.seq_lens),
+                    _ptr(self.page_table), N // PAGE if paged else 0,
+                    self.k.shape[0] if paged else 0, PAGE, HEAD_DIM, self.key_bits)
 
     def row_shape(self, last: int):
         """Shape of a per-token companion array (codes, scales, zeros)."""
@@ -597,11 +588,28 @@ def _on(device: torch.device, stream):
 
 
 def _need_on(t: torch.Tensor, dtype, name: str, device, shape=None):
-    _need(t, dtype, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _launch(f, where: str, device: torch.device, stream, *args) -> None:
+    """f(*args, stream) with the tensors' device current; `stream`, or that
+    device's current stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        st = torch.cuda.current_stream() if stream is None else stream
+        check(f(*args, st.cuda_stream), where)
+    else:
+        with torch.cuda.device(device):
+            st = torch.cuda.current_stream() if stream is None else stream
+            check(f(*args, st.cuda_stream), where)
 
 
 class PageTableUpdate:
@@ -647,13 +655,11 @@ class PageTableUpdate:
         _need_on(num_free, torch.int32, "num_free", self.device, (1,))
         if self.in_place:
             self.num_free_out = num_free
-        with _on(self.device, stream) as st:
-            check(lib.tw_update_page_table(
+        _launch(lib.tw_update_page_table, "tw_update_page_table", self.device, stream,
                 B, _ptr(self.seq_lens), _ptr(new_lens), _ptr(self.page_table), W, self.prefix_len,
                 _ptr(self.free_pages), self.free_pages.shape[0], _ptr(num_free),
                 _ptr(self.num_free_out), _ptr(self.seq_lens_out),
-                _ptr(self.slots) if self.num_slots else None, self.num_slots, _ptr(self.offsets),
-                st.cuda_stream), "tw_update_page_table")
+                _ptr(self.slots) if self.num_slots else None, self.num_slots, _ptr(self.offsets))
         return self
 
 
@@ -670,12 +676,12 @@ def update_page_table(seq_lens: torch.Tensor, new_lens: torch.Tensor, page_table
 def _token_rows(t: torch.Tensor, name: str, kv: KVCache, T: int) -> int:
     """Check new rows [T][Hk][128] (a slice of a wider projection may be given:
     only the last two dimensions must be packed).  Returns the token stride."""
-    if t.dtype != torch.float16 or t.device != kv.k.device or \
-            tuple(t.shape) != (T, kv.Hk, HEAD_DIM):
+    if t.dtype != torch.float16 or t.device != kv.k.device or t.shape != (T, kv.Hk, HEAD_DIM):
         raise ValueError(f"{name} must be fp16 [{T}][{kv.Hk}][128] on {kv.k.device}")
-    if t.stride(2) != 1 or (kv.Hk > 1 and t.stride(1) != HEAD_DIM):
+    st, sh, sd = t.stride()
+    if sd != 1 or (kv.Hk > 1 and sh != HEAD_DIM):
         raise ValueError(f"{name}: a token's heads must lie side by side")
-    stride = t.stride(0) if T > 1 else kv.Hk * HEAD_DIM
+    stride = st if T > 1 else kv.Hk * HEAD_DIM
     if stride < kv.Hk * HEAD_DIM or stride % 8:
         raise ValueError(f"{name}: token stride {stride} must be a multiple of 8, "
                          f"at least {kv.Hk * HEAD_DIM}")
@@ -707,11 +713,10 @@ def write_rows(kv: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: tor
     if T == 0:
         return
     s = kv.struct()
-    with _on(dev, stream) as st:
-        check(lib.tw_write_rows(
+    _launch(lib.tw_write_rows, "tw_write_rows", dev, stream,
             ctypes.byref(s), _ptr(k_new), ks, _ptr(v_new), vs, _ptr(slots), T,
             _ptr(keys.codes) if keys else None, _ptr(keys.scales) if keys else None,
-            _ptr(keys.zeros) if keys else None, _ptr(meta), st.cuda_stream), "tw_write_rows")
+            _ptr(keys.zeros) if keys else None, _ptr(meta))
 
 
 def prefix_workspace_bytes(B: int, Hq: int, Hk: int, prefix_len: int) -> int:
@@ -757,11 +762,9 @@ class PrefixDecodeStep:
         _need_on(q, torch.float16, "q", self.kv.k.device, (self.kv.B, self.Hq, HEAD_DIM))
         if self.kv.B == 0:
             return self.out
-        with _on(self.kv.k.device, stream) as st:
-            check(lib.tw_prefix_decode(
+        _launch(lib.tw_prefix_decode, "tw_prefix_decode", self.kv.k.device, stream,
                 _ptr(q), self.Hq, ctypes.byref(self._kvs), self.prefix_len, _ptr(self.out),
-                _ptr(self.lse), _ptr(self.ws), self.ws.numel(), st.cuda_stream),
-                "tw_prefix_decode")
+                _ptr(self.lse), _ptr(self.ws), self.ws.numel())
         return self.out
 
 

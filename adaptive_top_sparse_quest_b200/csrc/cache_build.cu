@@ -19,6 +19,11 @@
 
 namespace tw {
 
+// h_key of both halves of a word (its own inverse).
+__device__ __forceinline__ uint32_t h_key2(uint32_t w) {
+  return w ^ (((w >> 15) & 0x00010001u) * 0x7FFFu);
+}
+
 // Quantise one token row held by a half-warp (lane l16 holds channels
 // 8 l16 .. 8 l16 + 7 in `raw`) to BITS-bit codes (levels 0 .. 2^BITS - 1) and
 // store its codes, scales and zeros at `row`.  Every value is a fixed sequence
@@ -35,18 +40,18 @@ __device__ __forceinline__ void quantize_row(const uint4 raw, int64_t row, int l
   constexpr int kLevels = (1 << BITS) - 1;
   const int l16 = lane & 15;
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  int kmin = 0x7FFFFFFF, kmax = -0x7FFFFFFF - 1;
+  uint32_t lo = h_key2(w[0]), hi = lo;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int kk = h_key((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
-    kmin = min(kmin, kk);
-    kmax = max(kmax, kk);
+  for (int j = 1; j < 4; ++j) {
+    lo = __vmins2(lo, h_key2(w[j]));
+    hi = __vmaxs2(hi, h_key2(w[j]));
   }
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
-    kmin = min(kmin, __shfl_xor_sync(hmask, kmin, o));
-    kmax = max(kmax, __shfl_xor_sync(hmask, kmax, o));
+    lo = __vmins2(lo, __shfl_xor_sync(hmask, lo, o));
+    hi = __vmaxs2(hi, __shfl_xor_sync(hmask, hi, o));
   }
+  const int kmin = min((int)(int16_t)lo, (int)lo >> 16), kmax = max((int)(int16_t)hi, (int)hi >> 16);
   const uint32_t mn_bits = h_from_key(kmin);
   const uint32_t mx_bits = h_from_key(kmax);
   const float mnf = __half2float(__ushort_as_half((unsigned short)mn_bits));
@@ -54,16 +59,24 @@ __device__ __forceinline__ void quantize_row(const uint4 raw, int64_t row, int l
   const float s32 = __fdiv_rn(__fsub_rn(mxf, mnf), (float)kLevels);
   const __half sc = __float2half_rn(s32);
   const float scf = __half2float(sc);
+  // code = rint(fl((x - mn) / scale)).  The product y with the approximate
+  // reciprocal (off by 2^-23 of itself at most) is within 2^-22 of the rounded
+  // quotient, relative; quotients are below 32 (the levels, or 1.5 times as many
+  // where the scale is of fp16's smallest values and rounded down), so within
+  // 2^-17.  Only a y that is about that near to a half-integer can round to
+  // another code: those divide.
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scf));
+  if (scf == 0.0f) inv = 0.0f;   // all codes 0
   uint32_t packed = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float x =
         __half2float(__ushort_as_half((unsigned short)((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu)));
-    int c = 0;
-    if (scf != 0.0f) {
-      c = __float2int_rn(__fdiv_rn(__fsub_rn(x, mnf), scf));
-      c = min(max(c, 0), kLevels);
-    }
+    const float d = __fsub_rn(x, mnf);
+    float y = __fmul_rn(d, inv);
+    if (fabsf(y - rintf(y)) > 0.5f - 0x1p-15f) y = __fdiv_rn(d, scf);
+    const int c = min(max(__float2int_rn(y), 0), kLevels);
     packed |= (uint32_t)c << (BITS * j);
   }
   if (BITS == 4)
@@ -239,11 +252,11 @@ k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restric
     }
     const __half* ks = k_new + tok * k_stride + h * kHeadDim + l16 * 8;
     const __half* vs = v_new + tok * v_stride + h * kHeadDim + l16 * 8;
-    int kmin[8], kmax[8];
+    uint32_t kmin[4], kmax[4];   // keys of the lane's eight channels
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      kmin[j] = 0x7FFFFFFF;
-      kmax[j] = -0x7FFFFFFF - 1;
+    for (int j = 0; j < 4; ++j) {
+      kmin[j] = 0x7FFF7FFFu;
+      kmax[j] = 0x80008000u;
     }
     for (int c = 0; c < n; c += kWrRows) {
       uint4 kr[kWrRows], vr[kWrRows];
@@ -262,10 +275,9 @@ k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restric
           if (codes) quantize_row<BITS>(kr[x], at, lane, hmask, codes, scales, zeros);
           const uint32_t w[4] = {kr[x].x, kr[x].y, kr[x].z, kr[x].w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int kk = h_key((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
-            kmin[j] = min(kmin[j], kk);
-            kmax[j] = max(kmax[j], kk);
+          for (int j = 0; j < 4; ++j) {
+            kmin[j] = __vmins2(kmin[j], h_key2(w[j]));
+            kmax[j] = __vmaxs2(kmax[j], h_key2(w[j]));
           }
         }
     }
@@ -277,19 +289,15 @@ k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restric
       const uint32_t on[4] = {omn.x, omn.y, omn.z, omn.w};
       const uint32_t ox[4] = {omx.x, omx.y, omx.z, omx.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        kmin[j] = min(kmin[j], h_key((on[j >> 1] >> (16 * (j & 1))) & 0xFFFFu));
-        kmax[j] = max(kmax[j], h_key((ox[j >> 1] >> (16 * (j & 1))) & 0xFFFFu));
+      for (int j = 0; j < 4; ++j) {
+        kmin[j] = __vmins2(kmin[j], h_key2(on[j]));
+        kmax[j] = __vmaxs2(kmax[j], h_key2(ox[j]));
       }
     }
-    uint32_t mn[4], mx[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      mn[j] = h_from_key(kmin[2 * j]) | (h_from_key(kmin[2 * j + 1]) << 16);
-      mx[j] = h_from_key(kmax[2 * j]) | (h_from_key(kmax[2 * j + 1]) << 16);
-    }
-    *reinterpret_cast<uint4*>(dst) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
-    *reinterpret_cast<uint4*>(dst + kHeadDim) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(h_key2(kmin[0]), h_key2(kmin[1]), h_key2(kmin[2]), h_key2(kmin[3]));
+    *reinterpret_cast<uint4*>(dst + kHeadDim) =
+        make_uint4(h_key2(kmax[0]), h_key2(kmax[1]), h_key2(kmax[2]), h_key2(kmax[3]));
   }
 }
 

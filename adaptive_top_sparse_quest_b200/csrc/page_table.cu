@@ -39,10 +39,11 @@ struct PtSmem {
   // then int old_len[B], new_len[B], tok_end[B], give_end[B], take_end[B]
 };
 
-// Inclusive scan over the block's threads; *total gets the sum.
+// Inclusive scan over the block's threads; *total gets the sum.  Every warp
+// scans the warps' totals for itself.
 template <typename T>
 __device__ __forceinline__ T block_scan(T v, T* sh, T* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const T t = __shfl_up_sync(0xffffffffu, v, o);
@@ -51,14 +52,15 @@ __device__ __forceinline__ T block_scan(T v, T* sh, T* total) {
   __syncthreads();   // sh may still be read by an earlier scan
   if (lane == 31) sh[warp] = v;
   __syncthreads();
-  T before = 0, all = 0;
-  for (int w = 0; w < kPtThreads / 32; ++w) {
-    const T x = sh[w];
-    if (w < warp) before += x;
-    all += x;
+  T w = lane < nw ? sh[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T t = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += t;
   }
-  *total = all;
-  return v + before;
+  *total = __shfl_sync(0xffffffffu, w, nw - 1);
+  const T before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return v + (warp ? before : 0);
 }
 
 // First index whose (ascending) end is above x; n if none.
@@ -83,13 +85,13 @@ __global__ void __launch_bounds__(kPtThreads) k_update_page_table(PtArgs a) {
   int* give_end = tok_end + a.B;
   int* take_end = give_end + a.B;
   const int tid = threadIdx.x;
-  const int nt = (int)cluster_size() * kPtThreads, gt = (int)cluster_rank() * kPtThreads + tid;
+  const int nth = blockDim.x, nt = (int)cluster_size() * nth, gt = (int)cluster_rank() * nth + tid;
   const int room = a.W * kPage;
   auto pages = [&](int n) { return max((n + kPage - 1) / kPage, a.keep); };
 
   const int F = max(0, min(*a.num_free, a.cap));
   // thread t owns the per consecutive sequences from t * per
-  const int per = (a.B + kPtThreads - 1) / kPtThreads;
+  const int per = (a.B + nth - 1) / nth;
   int64_t tok[kPtPer], tok_sum = 0, tok_all;
   int give[kPtPer], give_sum = 0, give_all;
 #pragma unroll
@@ -171,21 +173,38 @@ __global__ void __launch_bounds__(kPtThreads) k_update_page_table(PtArgs a) {
   // a slot per new token; the page of a token past the old ones is read from
   // the stack, not from the table entry that another thread may be writing
   if (a.slots) {
-    for (int i = gt; i < a.num_slots; i += nt) {
-      const int b = upper(tok_end, a.B, i);
-      int slot = -1;
-      if (b < a.B && served(b)) {
-        const int o = old_len[b], pos = o + i - (b ? tok_end[b - 1] : 0);
-        const int pg = pos / kPage, have = pages(o);
-        if (pg >= a.keep) {
-          const int p = pg < have
-                            ? a.page_table[(int64_t)b * a.W + pg]
-                            : __ldcg(a.free_pages + avail - 1 -
-                                     ((b ? take_end[b - 1] : 0) + pg - have));
-          if ((unsigned)p < (unsigned)a.cap) slot = p * kPage + pos % kPage;
+    // runs of four places per thread: one search for the sequence of the first
+    for (int i0 = 4 * gt; i0 < a.num_slots; i0 += 4 * nt) {
+      int b = upper(tok_end, a.B, i0);
+      const int n = min(4, a.num_slots - i0);
+      int out[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j;
+        int slot = -1;
+        if (j < n) {
+          if (b < a.B && tok_end[b] <= i) b = upper(tok_end, a.B, i);
+          if (b < a.B && served(b)) {
+            const int o = old_len[b], pos = o + i - (b ? tok_end[b - 1] : 0);
+            const int pg = pos / kPage, have = pages(o);
+            if (pg >= a.keep) {
+              const int p = pg < have
+                                ? a.page_table[(int64_t)b * a.W + pg]
+                                : __ldcg(a.free_pages + avail - 1 -
+                                         ((b ? take_end[b - 1] : 0) + pg - have));
+              if ((unsigned)p < (unsigned)a.cap) slot = p * kPage + pos % kPage;
+            }
+          }
         }
+        out[j] = slot;
       }
-      a.slots[i] = slot;
+      if (n == 4 && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
+        *reinterpret_cast<int4*>(a.slots + i0) = make_int4(out[0], out[1], out[2], out[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < n) a.slots[i0 + j] = out[j];
+      }
     }
   }
 }
@@ -199,9 +218,12 @@ cudaError_t launch_update_page_table(const PtArgs& a, cudaStream_t st) {
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int ctas = a.B + (int64_t)a.num_slots > 4 * kPtThreads ? 8 : 1;
+  // a small batch on one small block: its barriers cost least; a large one on
+  // a cluster of eight
+  const int64_t work = a.B + (int64_t)a.num_slots;
+  const int ctas = work > 4 * kPtThreads ? 8 : 1;
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kPtThreads);
+  cfg.blockDim = dim3(work > 1024 ? kPtThreads : 256);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
