@@ -74,10 +74,14 @@ __device__ __forceinline__ void quantize_row(const uint4 raw, int64_t row, int l
     const float x =
         __half2float(__ushort_as_half((unsigned short)((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu)));
     const float d = __fsub_rn(x, mnf);
-    float y = __fmul_rn(d, inv);
-    if (fabsf(y - rintf(y)) > 0.5f - 0x1p-15f) y = __fdiv_rn(d, scf);
-    const int c = min(max(__float2int_rn(y), 0), kLevels);
-    packed |= (uint32_t)c << (BITS * j);
+    // 1.5 * 2^23 + y rounds y to the nearest integer, ties to even, in its low bits
+    float y = __fmul_rn(d, inv), z = __fadd_rn(y, 12582912.0f);
+    if (fabsf(__fsub_rn(y, __fsub_rn(z, 12582912.0f))) > 0.5f - 0x1p-15f) {
+      y = __fdiv_rn(d, scf);
+      z = __fadd_rn(y, 12582912.0f);
+    }
+    const uint32_t c = min(__float_as_uint(z) - 0x4B400000u, (uint32_t)kLevels);
+    packed |= c << (BITS * j);
   }
   if (BITS == 4)
     *reinterpret_cast<uint32_t*>(codes + row * (kHeadDim / 2) + l16 * 4) = packed;
@@ -185,17 +189,18 @@ k_append_keys(Layout L, const __half* __restrict__ K, uint8_t* __restrict__ code
 // slots[t] names; in the same pass over the key row it is quantised, and the
 // page's min / max is folded, so K is read once instead of three times.
 //
-// A run of list neighbours on consecutive slots of one page is one half-warp's
-// work per KV head: it alone touches that page's metadata, so no atomics are
+// A run of list neighbours on consecutive slots of one page is one warp's work
+// per KV head, a row per half-warp at a time: it alone touches that page's metadata, so no atomics are
 // needed and the result does not depend on an order.  The run that starts at a
 // page's first row starts its metadata anew; another folds what is there (its
 // earlier rows are in it).  A block looks at `chunk` list places and takes the
 // runs that start there, to their ends up to 15 places further on.
 constexpr int kWrThreads = 256;
-constexpr int kWrRows = 4;   // rows of a run in flight per half-warp
+constexpr int kWrHeads = 16;  // KV heads per block
+constexpr int kWrRows = 2;   // rows of a run in flight per half-warp
 
 template <int BITS>
-__global__ void __launch_bounds__(kWrThreads)
+__global__ void __launch_bounds__(kWrThreads, 4)
 k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restrict__ v_new,
              int64_t k_stride, int64_t v_stride, const int32_t* __restrict__ slots, int T,
              int chunk, __half* __restrict__ K, __half* __restrict__ V,
@@ -231,9 +236,10 @@ k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restric
     }
   }
   __syncthreads();
-  const int h0 = blockIdx.y * (kWrThreads / 16);
-  const int nh = min(kWrThreads / 16, L.Hk - h0);
-  for (int i = tid >> 4; i < nruns * nh; i += kWrThreads / 16) {
+  const int h0 = blockIdx.y * kWrHeads;
+  const int nh = min(kWrHeads, L.Hk - h0);
+  const int hw = lane >> 4;
+  for (int i = tid >> 5; i < nruns * nh; i += kWrThreads / 32) {
     const int r = i / nh, h = h0 + i % nh;
     const int n = run_n[r], s = sl[run_at[r] + 1];
     const int64_t tok = t0 + run_at[r];
@@ -258,18 +264,18 @@ k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restric
       kmin[j] = 0x7FFF7FFFu;
       kmax[j] = 0x80008000u;
     }
-    for (int c = 0; c < n; c += kWrRows) {
+    for (int c = hw; c < n; c += 2 * kWrRows) {
       uint4 kr[kWrRows], vr[kWrRows];
 #pragma unroll
       for (int x = 0; x < kWrRows; ++x)
-        if (c + x < n) {
-          kr[x] = ld_stream16(ks + (c + x) * k_stride);
-          vr[x] = ld_stream16(vs + (c + x) * v_stride);
+        if (c + 2 * x < n) {
+          kr[x] = ld_stream16(ks + (c + 2 * x) * k_stride);
+          vr[x] = ld_stream16(vs + (c + 2 * x) * v_stride);
         }
 #pragma unroll
       for (int x = 0; x < kWrRows; ++x)
-        if (c + x < n) {
-          const int64_t at = row + c + x;
+        if (c + 2 * x < n) {
+          const int64_t at = row + c + 2 * x;
           *reinterpret_cast<uint4*>(K + at * kHeadDim + l16 * 8) = kr[x];
           *reinterpret_cast<uint4*>(V + at * kHeadDim + l16 * 8) = vr[x];
           if (codes) quantize_row<BITS>(kr[x], at, lane, hmask, codes, scales, zeros);
@@ -282,22 +288,25 @@ k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restric
         }
     }
     if (!meta) continue;
-    __half* dst = meta + mrec * (2 * kHeadDim) + l16 * 8;
-    if (o != 0) {
-      const uint4 omn = *reinterpret_cast<const uint4*>(dst);
-      const uint4 omx = *reinterpret_cast<const uint4*>(dst + kHeadDim);
-      const uint32_t on[4] = {omn.x, omn.y, omn.z, omn.w};
-      const uint32_t ox[4] = {omx.x, omx.y, omx.z, omx.w};
+    // fold the two halves' rows; one half then keeps the minima, the other the maxima
+    __syncwarp();
+    uint32_t m[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        kmin[j] = __vmins2(kmin[j], h_key2(on[j]));
-        kmax[j] = __vmaxs2(kmax[j], h_key2(ox[j]));
-      }
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = __vmins2(kmin[j], __shfl_xor_sync(0xffffffffu, kmin[j], 16));
+      const uint32_t hi = __vmaxs2(kmax[j], __shfl_xor_sync(0xffffffffu, kmax[j], 16));
+      m[j] = hw ? hi : lo;
+    }
+    __half* dst = meta + (mrec * 2 + hw) * kHeadDim + l16 * 8;
+    if (o != 0) {
+      const uint4 old = *reinterpret_cast<const uint4*>(dst);
+      const uint32_t ow[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        m[j] = hw ? __vmaxs2(m[j], h_key2(ow[j])) : __vmins2(m[j], h_key2(ow[j]));
     }
     *reinterpret_cast<uint4*>(dst) =
-        make_uint4(h_key2(kmin[0]), h_key2(kmin[1]), h_key2(kmin[2]), h_key2(kmin[3]));
-    *reinterpret_cast<uint4*>(dst + kHeadDim) =
-        make_uint4(h_key2(kmax[0]), h_key2(kmax[1]), h_key2(kmax[2]), h_key2(kmax[3]));
+        make_uint4(h_key2(m[0]), h_key2(m[1]), h_key2(m[2]), h_key2(m[3]));
   }
 }
 
@@ -390,7 +399,7 @@ cudaError_t launch_write_rows(const Layout& L, const __half* k_new, const __half
   // would not give every SM two blocks (single tokens are a run each)
   int chunk = kWrMaxChunk;
   while (chunk > 1 && (T + chunk - 1) / chunk < 2 * num_sms) chunk /= 2;
-  const dim3 grid((T + chunk - 1) / chunk, (L.Hk + kWrThreads / 16 - 1) / (kWrThreads / 16));
+  const dim3 grid((T + chunk - 1) / chunk, (L.Hk + kWrHeads - 1) / kWrHeads);
   return launch_k(L.kbits == 2 ? k_write_rows<2> : k_write_rows<4>, grid, dim3(kWrThreads), 0, st,
                   false, L, k_new, v_new, k_stride, v_stride, slots, T, chunk, K, V, codes, scales,
                   zeros, meta);

@@ -36,7 +36,6 @@ constexpr int kPtPer = kPtMaxBatch / kPtThreads;   // sequences per thread in th
 struct PtSmem {
   int64_t scan64[32];
   int scan32[32];
-  // then int old_len[B], new_len[B], tok_end[B], give_end[B], take_end[B]
 };
 
 // Inclusive scan over the block's threads; *total gets the sum.  Every warp
@@ -76,14 +75,30 @@ __device__ __forceinline__ int upper(const int* end, int n, int x) {
   return lo;
 }
 
+// The same by a whole warp, 32 probes at a time.
+__device__ __forceinline__ int upper_warp(const int* end, int n, int x) {
+  int lo = 0;
+  while (n > 0) {   // the answer lies in [lo, lo + n]
+    const int step = (n + 31) / 32, at = (threadIdx.x & 31) * step + step - 1;
+    const unsigned above = __ballot_sync(0xffffffffu, at < n && end[lo + at] > x);
+    // the first group whose last end is above x, or what is left past the last whole group
+    const int grp = above ? __ffs(above) - 1 : n / step;
+    lo += grp * step;
+    n = above ? step - 1 : n - grp * step;
+    if (!above && n == 0) break;
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(kPtThreads) k_update_page_table(PtArgs a) {
   extern __shared__ __align__(16) unsigned char pt_smem[];
   PtSmem& sm = *reinterpret_cast<PtSmem*>(pt_smem);
+  // four words per sequence, which later hold its record; then its last place + 1
   int* old_len = reinterpret_cast<int*>(pt_smem + sizeof(PtSmem));
   int* new_len = old_len + a.B;
-  int* tok_end = new_len + a.B;
-  int* give_end = tok_end + a.B;
+  int* give_end = new_len + a.B;
   int* take_end = give_end + a.B;
+  int* tok_end = take_end + a.B;
   const int tid = threadIdx.x;
   const int nth = blockDim.x, nt = (int)cluster_size() * nth, gt = (int)cluster_rank() * nth + tid;
   const int room = a.W * kPage;
@@ -147,7 +162,10 @@ __global__ void __launch_bounds__(kPtThreads) k_update_page_table(PtArgs a) {
     if (F + i < a.cap)
       a.free_pages[F + i] = a.page_table[(int64_t)b * a.W + pages(new_len[b]) + at];
   }
-  cluster_sync();
+  if (cluster_size() > 1)
+    cluster_sync();
+  else
+    __syncthreads();
 
   // a growth is served when the stack holds its pages and all before them
   auto served = [&](int b) {
@@ -170,41 +188,69 @@ __global__ void __launch_bounds__(kPtThreads) k_update_page_table(PtArgs a) {
     a.offsets[0] = 0;
     *a.num_free_out = avail - used;
   }
-  // a slot per new token; the page of a token past the old ones is read from
-  // the stack, not from the table entry that another thread may be writing
-  if (a.slots) {
-    // runs of four places per thread: one search for the sequence of the first
-    for (int i0 = 4 * gt; i0 < a.num_slots; i0 += 4 * nt) {
-      int b = upper(tok_end, a.B, i0);
-      const int n = min(4, a.num_slots - i0);
-      int out[4];
+  if (!a.slots) return;
+  // what a place needs of its sequence, as one record: first place, old length
+  // (below 0: no growth served), place on the stack of its first new page, old pages
+  __syncthreads();
+  int4 rec[kPtPer];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j;
-        int slot = -1;
-        if (j < n) {
-          if (b < a.B && tok_end[b] <= i) b = upper(tok_end, a.B, i);
-          if (b < a.B && served(b)) {
-            const int o = old_len[b], pos = o + i - (b ? tok_end[b - 1] : 0);
-            const int pg = pos / kPage, have = pages(o);
-            if (pg >= a.keep) {
-              const int p = pg < have
-                                ? a.page_table[(int64_t)b * a.W + pg]
-                                : __ldcg(a.free_pages + avail - 1 -
-                                         ((b ? take_end[b - 1] : 0) + pg - have));
-              if ((unsigned)p < (unsigned)a.cap) slot = p * kPage + pos % kPage;
-            }
-          }
+  for (int j = 0; j < kPtPer; ++j) {
+    const int b = tid * per + j;
+    if (j < per && b < a.B)
+      rec[j] = make_int4(b ? tok_end[b - 1] : 0, served(b) ? old_len[b] : -1,
+                         avail - 1 - (b ? take_end[b - 1] : 0), pages(old_len[b]));
+  }
+  __syncthreads();
+  int4* recs = reinterpret_cast<int4*>(old_len);
+#pragma unroll
+  for (int j = 0; j < kPtPer; ++j) {
+    const int b = tid * per + j;
+    if (j < per && b < a.B) recs[b] = rec[j];
+  }
+  __syncthreads();
+  // runs of four places per thread, the last threads first (the first ones have
+  // the pages to move); a warp's 128 places span few sequences, which its lanes
+  // find together
+  const int lane = tid & 31;
+  for (int64_t w0 = 128 * (int64_t)((nt - 1 - gt) >> 5); w0 < a.num_slots; w0 += 4 * nt) {
+    const int b_lo = upper_warp(tok_end, a.B, (int)w0);
+    const int last = (int)min(w0 + 127, (int64_t)a.num_slots - 1);
+    const int b_hi = b_lo < a.B && tok_end[b_lo] <= last ? upper_warp(tok_end, a.B, last) : b_lo;
+    const int i0 = (int)w0 + 4 * lane;
+    if (i0 >= a.num_slots) continue;
+    int b = b_lo + upper(tok_end + b_lo, b_hi - b_lo, i0);
+    const int n = min(4, a.num_slots - i0);
+    // where each place's page id stands, then the four loads at once (a page past
+    // the old ones from the stack, not from the table entry being written)
+    const int32_t* src[4];
+    int row[4], out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j;
+      src[j] = nullptr;
+      row[j] = 0;
+      if (b < b_hi && tok_end[b] <= i) b += upper(tok_end + b, b_hi - b, i);
+      if (j < n && b < a.B) {
+        const int4 r = recs[b];
+        if (i < tok_end[b] && r.y >= 0) {
+          const int pos = r.y + i - r.x, pg = pos / kPage;
+          row[j] = pos % kPage;
+          if (pg >= a.keep)
+            src[j] = pg < r.w ? a.page_table + (int64_t)b * a.W + pg : a.free_pages + r.z - (pg - r.w);
         }
-        out[j] = slot;
       }
-      if (n == 4 && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
-        *reinterpret_cast<int4*>(a.slots + i0) = make_int4(out[0], out[1], out[2], out[3]);
-      } else {
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < n) a.slots[i0 + j] = out[j];
-      }
+    for (int j = 0; j < 4; ++j) out[j] = src[j] ? __ldcg(src[j]) : -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      out[j] = (unsigned)out[j] < (unsigned)a.cap ? out[j] * kPage + row[j] : -1;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
+      *reinterpret_cast<int4*>(a.slots + i0) = make_int4(out[0], out[1], out[2], out[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) a.slots[i0 + j] = out[j];
     }
   }
 }
