@@ -767,7 +767,7 @@ int tw_prefix_decode(const uint16_t* q, int32_t num_q_heads, const tw_kv* kv, in
   const int64_t nrows = L.page_table ? (int64_t)L.pool_pages * L.Hk * tw::kPage
                                      : (int64_t)L.B * L.Hk * L.N;
   if (nrows > INT32_MAX || (int64_t)L.B * num_q_heads > INT32_MAX / tw::kHeadDim ||
-      (int64_t)L.B * num_q_heads * ((int64_t)L.N / 128 + 1) > INT32_MAX)
+      (int64_t)L.B * num_q_heads * ((int64_t)L.N / 128 + 2) > INT32_MAX / 16)
     return TW_ERR_UNSUPPORTED;
   if (L.B == 0) return TW_OK;
   TW_TRY(check_ws(ws, ws_bytes,

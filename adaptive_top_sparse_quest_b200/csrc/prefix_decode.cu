@@ -92,7 +92,7 @@ struct PdArgs {
   float2* ml1;                  // [slot][rows1] (m, l)
   float* o2;                    // [slot][G][128]
   float2* ml2;
-  int* cum;                     // [B + 1] own key tiles before each sequence
+  uint64_t* cum;                // [B + 1] sequences with own tiles (high half) and own tiles before each
   PdRange* ranges;              // [kPdCtas]
   int* status;
   __half* out;
@@ -100,9 +100,9 @@ struct PdArgs {
 };
 
 struct PdCtl {
-  uint64_t kfull[2], vfull[2], kempty[2], vempty[2], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], shared_done, drain;
+  uint64_t kfull[2], vfull[2], kempty[2], vempty[2], qfull[2], qempty[2], sfull[2], pfull[2], phalf[2], ofull[2], shared_done, drain;
   uint32_t tmem;
-  int red[kPdThreads / 32];
+  uint64_t red[kPdThreads / 32];
   PdRange range;
   int at_b[2], at_h[2], at_t[2];   // where each stream's own tiles begin
 };
@@ -115,6 +115,33 @@ constexpr size_t kPdSmem = 6 * kBuf + kPdCtlBytes + 8 * 4096 + 1024;
 __device__ __forceinline__ int own_tiles(const PdArgs& a, int b) {
   const int n = a.L.len(b) - a.P;
   return n > 0 ? (n + kTile - 1) / kTile : 0;
+}
+
+// The CTAs share the tiles out by cost, on one line: the prefix's units, each a
+// start (query rows, record) and KT tiles, then the own parts' units (sequence
+// by sequence, head by head) likewise.  Costs are in sixths of the time of a
+// tile that only waits for its copy; a pair's tile of 256 query rows takes half
+// as long again.  (64 sequences behind 32k tokens: 59 us, 68 with every tile
+// alike; 16 of a multi-head layer, many short units: 41 us, 47 without starts.)
+constexpr int kOwnCost = 6, kOwnStart = 2, kUnitStart = 12;
+__device__ __forceinline__ int tile_cost(const PdArgs& a) { return a.pair ? 9 : 6; }
+__device__ __forceinline__ int unit_span(const PdArgs& a) {
+  return a.KT * tile_cost(a) + kUnitStart;
+}
+__device__ __forceinline__ int64_t prefix_span(const PdArgs& a) {
+  return a.KT > 0 ? (int64_t)a.L.Hk * a.RT * unit_span(a) : 0;
+}
+// Cost per KV head of (sequences, own tiles).
+__device__ __forceinline__ int64_t own_cost(uint64_t v) {
+  return (int64_t)(v >> 32) * kOwnStart + (int64_t)(uint32_t)v * kOwnCost;
+}
+// First prefix tile that lies at x or after it.
+__device__ __forceinline__ int prefix_tile_at(const PdArgs& a, int64_t x) {
+  if (x <= 0) return 0;
+  const uint32_t span = unit_span(a);
+  const int64_t u = (uint64_t)x >> 32 ? x / span : (uint32_t)x / span;
+  const int in = (int)(x - u * span) - kUnitStart, cost = tile_cost(a);
+  return (int)(u * a.KT) + (in <= 0 ? 0 : (in + cost - 1) / cost);
 }
 
 // A run of consecutive key tiles of one unit, on one stream.
@@ -221,19 +248,21 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       mbar_init(&c.qempty[i], 1);
       mbar_init(&c.sfull[i], 1);
       mbar_init(&c.pfull[i], 4);
+      mbar_init(&c.phalf[i], 4);
       mbar_init(&c.ofull[i], 1);
     }
     mbar_init(&c.shared_done, 1);
     mbar_init(&c.drain, 2);
     mbar_fence_init();
   }
-  // own key tiles of all sequences, this CTA's share of all tiles, and where in
-  // the list of sequences its own tiles begin
+  // own key tiles of all sequences, this CTA's stretch of the line of costs, and
+  // the tiles at its ends and its middle
   {
-    auto block_incl = [&](int v, int* all) {   // inclusive sum over the block
+    // inclusive sum over the block of (sequences with own tiles, own tiles), 32 bits each
+    auto block_incl = [&](uint64_t v, uint64_t* all) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        const uint64_t t = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += t;
       }
       if (lane == 31) c.red[warp] = v;
@@ -241,48 +270,67 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       *all = 0;
 #pragma unroll
       for (int w = 0; w < kPdThreads / 32; ++w) {
-        const int x = c.red[w];
+        const uint64_t x = c.red[w];
         if (w < warp) v += x;
         *all += x;
       }
       return v;
     };
-    int sum = 0, total;
-    for (int b = tid; b < a.L.B; b += kPdThreads) sum += own_tiles(a, b);
-    const int incl0 = block_incl(sum, &total);
-    const int64_t S1 = (int64_t)a.L.Hk * a.RT * a.KT, X = S1 + (int64_t)total * a.L.Hk;
+    auto tiles_of = [&](int b) {
+      const int kt = own_tiles(a, b);
+      return kt > 0 ? (1ull << 32) | (uint64_t)kt : 0ull;
+    };
+    uint64_t sum = 0, total;
+    for (int b = tid; b < a.L.B; b += kPdThreads) sum += tiles_of(b);
+    const uint64_t incl0 = block_incl(sum, &total);
+    const int64_t X1 = prefix_span(a), X = X1 + own_cost(total) * a.L.Hk;
     const int64_t x0 = X * blockIdx.x / kPdCtas, x1 = X * (blockIdx.x + 1) / kPdCtas;
-    PdRange r;
-    r.p0 = (int)min(x0, S1);
-    r.p1 = (int)min(x1, S1);
-    r.s0 = (int)(max(x0, S1) - S1);
-    r.s1 = (int)(max(x1, S1) - S1);
-    // an odd tile goes to stream 0, of both parts to one stream each
-    r.pm = r.p0 + (r.p1 - r.p0 + 1) / 2;
-    r.sm = r.s0 + (r.s1 - r.s0 + (!a.pair && ((r.p1 - r.p0) & 1) ? 0 : 1)) / 2;
+    // paired streams share the prefix's tiles and halve the own ones; others halve
+    // the whole stretch
+    const int64_t xm = a.pair ? (max(x0, X1) + max(x1, X1)) / 2 : (x0 + x1) / 2;
+    const int64_t at[3] = {max(x0, X1) - X1, max(xm, X1) - X1, max(x1, X1) - X1};
     if (tid == 0) {
+      PdRange r;
+      r.p0 = prefix_tile_at(a, min(x0, X1));
+      r.p1 = prefix_tile_at(a, min(x1, X1));
+      r.pm = a.pair ? r.p1 : prefix_tile_at(a, min(xm, X1));
+      r.s0 = r.sm = r.s1 = (int)(uint32_t)total * a.L.Hk;   // past the last, unless found below
       c.range = r;
-      a.ranges[blockIdx.x] = r;
     }
-    int before = 0;
+    __syncthreads();
+    uint64_t before = 0;
     for (int b0 = 0; b0 < a.L.B; b0 += kPdThreads) {
       const int b = b0 + tid;
-      int kt = sum, incl = incl0, chunk = total;
+      uint64_t mine = sum, incl = incl0, chunk = total;
       if (a.L.B > kPdThreads) {   // else the sums above are these
-        kt = b < a.L.B ? own_tiles(a, b) : 0;
+        mine = b < a.L.B ? tiles_of(b) : 0;
         __syncthreads();
-        incl = block_incl(kt, &chunk);
+        incl = block_incl(mine, &chunk);
       }
-      const int first = before + incl - kt;
+      const uint64_t first = before + incl - mine;
       if (blockIdx.x == 0 && b < a.L.B) a.cum[b] = first;
-      const int64_t lo = (int64_t)first * a.L.Hk;
+      const int kt = (int)(uint32_t)mine, cost = (int)own_cost(mine);
+      const int64_t lo = own_cost(first) * a.L.Hk;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t s = (i == 0 ? r.s0 : r.sm) - lo;
-        if (kt > 0 && s >= 0 && s < (int64_t)kt * a.L.Hk) {
-          c.at_b[i] = b;
-          c.at_h[i] = (int)s / kt;
-          c.at_t[i] = (int)s % kt;
+      for (int k = 0; k < 3; ++k) {
+        const int64_t off = at[k] - lo;
+        if (off >= 0 && off < (int64_t)cost * a.L.Hk) {
+          int h = (int)off / cost;
+          const int in = (int)off - h * cost - kOwnStart;
+          int t = in <= 0 ? 0 : (in + kOwnCost - 1) / kOwnCost;
+          const int tile = (int)(uint32_t)first * a.L.Hk + h * kt + t;
+          if (t == kt) {   // the next unit's start
+            t = 0;
+            ++h;
+          }
+          if (k == 0) c.range.s0 = tile;
+          if (k == 1) c.range.sm = tile;
+          if (k == 2) c.range.s1 = tile;
+          if (k < 2) {
+            c.at_b[k] = h == a.L.Hk ? b + 1 : b;
+            c.at_h[k] = h == a.L.Hk ? 0 : h;
+            c.at_t[k] = t;
+          }
         }
       }
       before += chunk;
@@ -291,6 +339,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0) a.ranges[blockIdx.x] = c.range;
   }
   const uint32_t tmem = uni(c.tmem);
   const int pairs = a.pair ? c.range.p1 - c.range.p0 : 0;   // tiles on shared buffers
@@ -361,15 +410,16 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       umma_ss4(s_col, qd + (kBlk >> 4), kd + (kBlk >> 4), id, 1);
       umma_commit(&c.sfull[i]);
     };
-    auto issue_o = [&](const int i, uint32_t set, uint32_t np, uint32_t more) {   // O += P V
+    // O += P V, the first or second 64 keys: the first while the softmax is at the others
+    auto issue_o = [&](const int i, uint32_t set, uint32_t np, uint32_t more, const int half) {
       const uint32_t s_col = tmem + i * kTile, o_col = tmem + 2 * kTile + i * kTile;
       const uint64_t vd = umma_desc(v_buf(set), kBlk, 1024);
       const uint32_t id = umma_idesc(kHeadDim, true);
-      if (np == kTilePages) {
-        umma_ts4(o_col, s_col, vd, id, more);
-        umma_ts4(o_col, s_col + 32, vd + 4 * (2048 >> 4), id, 1);
+      const uint32_t y0 = half * (kTilePages / 2), y1 = half ? np : min(np, (uint32_t)kTilePages / 2);
+      if (y1 == y0 + kTilePages / 2) {
+        umma_ts4(o_col, s_col + half * 32, vd + half * 4 * (2048 >> 4), id, half ? 1 : more);
       } else {
-        for (uint32_t y = 0; y < np; ++y)
+        for (uint32_t y = y0; y < y1; ++y)
           umma_ts(o_col, s_col + y * 8, vd + y * (2048 >> 4), id, more | y);
       }
     };
@@ -405,10 +455,14 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
             ok = mbar_wait(&c.vfull[set], (k >> 1) & 1, a.status);
             if (!ok) break;
             for (int j = 0; j < 1 + (int)two; ++j) {
+              ok = mbar_wait(&c.phalf[j], (j ? nt1 + x : nt + x) & 1, a.status);
+              if (!ok) break;
+              tc_fence_after();
+              issue_o(j, set, np, more, 0);
               ok = mbar_wait(&c.pfull[j], (j ? nt1 + x : nt + x) & 1, a.status);
               if (!ok) break;
               tc_fence_after();
-              issue_o(j, set, np, more);
+              issue_o(j, set, np, more, 1);
               umma_commit(&c.vempty[set]);
               if (!two) umma_commit(&c.vempty[set]);
               if (last) {
@@ -467,10 +521,14 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
           fence_async_proxy();
           __syncwarp();
         }
+        ok = mbar_wait(&c.phalf[i], nt & 1, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        issue_o(i, i, np, more, 0);
         ok = mbar_wait(&c.pfull[i], nt & 1, a.status);
         if (!ok) break;
         tc_fence_after();
-        issue_o(i, i, np, more);
+        issue_o(i, i, np, more, 1);
         umma_commit(&c.vempty[i]);
         umma_commit(&c.vempty[i]);
         if (last) umma_commit(&c.ofull[i]);
@@ -555,6 +613,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         ok = mbar_wait(&c.sfull[i], nt & 1, a.status);
         if (!ok) break;
         tc_fence_after();
+        bool half = false;   // the first 64 keys' weights are handed over
         if (busy) {
           const int ncol = lim - (g.t0 + x) * kTile;   // keys of the tile this row sees
           if (__all_sync(0xffffffffu, ncol >= kTile)) {
@@ -578,6 +637,13 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
               tmem_use32(s[y & 1]);
               if (y < 3) tmem_ld32(s_col + 32 * (y + 1), s[(y + 1) & 1]);
               weights32(s[y & 1], y, lift);   // over scores read already
+              if (y == 1) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.phalf[i]);
+                half = true;
+              }
             }
           } else {
             // a tile that ends early, for some row at least: chunk by chunk,
@@ -610,7 +676,10 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.pfull[i]);
+        if (lane == 0) {
+          if (!half) mbar_arrive(&c.phalf[i]);
+          mbar_arrive(&c.pfull[i]);
+        }
       }
       if (!ok) break;
       ok = mbar_wait(&c.ofull[i], nseg & 1, a.status);
@@ -678,77 +747,101 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
   griddep_wait();
   if (W < kJoinWarps && bh >= (int64_t)a.L.B * a.Hq) return;
   const int b = (int)(bh / a.Hq), hq = (int)(bh % a.Hq), h = hq / a.G, g = hq % a.G;
-  const int64_t S1 = (int64_t)a.L.Hk * a.RT * a.KT;
-  const int len = a.L.len(b), total = __ldcg(a.cum + a.L.B), c0 = __ldcg(a.cum + b),
-            n2 = __ldcg(a.cum + b + 1) - c0;
-  const int64_t X = S1 + (int64_t)total * a.L.Hk;
-  // tile x of all X lies with CTA floor(x kPdCtas / X) or, after rounding, a
-  // neighbour; the CTAs' own ranges decide
-  const float per_tile = (float)kPdCtas / (float)max(X, (int64_t)1);
+  const int len = a.L.len(b);
+  const uint64_t total = __ldcg(a.cum + a.L.B), c0 = __ldcg(a.cum + b), c1 = __ldcg(a.cum + b + 1);
+  const int64_t X1 = prefix_span(a), X = X1 + own_cost(total) * a.L.Hk;
+  // what lies at x is CTA floor(x kPdCtas / X)'s or, after rounding, a
+  // neighbour's; the CTAs' own ranges decide
+  const float per_x = (float)kPdCtas / (float)max(X, (int64_t)1);
+  // Records of tiles [first, first + n) of the prefix's (part 0) or the own
+  // (part 1) list, written to slot worker + u, row `row` of `per`; the workers
+  // nw that may have some
+  struct Part {
+    int64_t u, first;
+    int n, per, row, split, c_lo, nw;
+  } p[2];
+  const int m = b * a.G + g;
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    Part& q = p[part];
+    int64_t x0, x1;
+    if (part == 0) {
+      q.n = len > 0 ? a.KT : 0;
+      q.u = (int64_t)h * a.RT + (a.pair ? m / (2 * kTile) : 0);
+      q.first = q.u * a.KT;
+      q.per = a.rows1;
+      q.row = a.pair ? m % (2 * kTile) : m;
+      q.split = a.pair ? 1 : 2;   // records per CTA at most
+      x0 = q.u * unit_span(a);
+      x1 = x0 + unit_span(a);
+    } else {
+      q.n = (int)(uint32_t)(c1 - c0);
+      q.u = (int64_t)b * a.L.Hk + h;
+      q.first = (int64_t)(uint32_t)c0 * a.L.Hk + (int64_t)h * q.n;
+      q.per = a.G;
+      q.row = g;
+      q.split = 2;
+      x0 = X1 + own_cost(c0) * a.L.Hk + h * own_cost(c1 - c0);
+      x1 = x0 + own_cost(c1 - c0);
+    }
+    q.c_lo = max(0, (int)((float)x0 * per_x) - 1);
+    const int c_hi = min(kPdCtas - 1, (int)((float)x1 * per_x) + 1);
+    q.nw = q.n > 0 ? (c_hi - q.c_lo + 1) * q.split : 0;
+  }
   float M = -INFINITY, Ls = 0.f;
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
-    // records of tiles [first, first + n) of the prefix's (part 0) or the own
-    // (part 1) list, written to slot worker + u, row `row` of `per`
-    const int n = part ? n2 : len > 0 ? a.KT : 0;
-    if (n == 0) continue;
-    const int m = b * a.G + g;
-    const int64_t u = part ? (int64_t)b * a.L.Hk + h
-                           : (int64_t)h * a.RT + (a.pair ? m / (2 * kTile) : 0);
-    const int64_t first = part ? (int64_t)c0 * a.L.Hk + (int64_t)h * n : u * a.KT;
-    const int per = part ? a.G : a.rows1, row = part ? g : a.pair ? m % (2 * kTile) : m;
-    const int split = part == 0 && a.pair ? 1 : 2;   // records per CTA at most
-    const int64_t x0 = first + (part ? S1 : 0);
-    const int c_lo = max(0, (int)((float)x0 * per_tile) - 1);
-    const int c_hi = min(kPdCtas - 1, (int)((float)(x0 + n) * per_tile) + 1);
-    const int nw = (c_hi - c_lo + 1) * split;
-    const float2* ml = part ? a.ml2 : a.ml1;
-    const float4* o = reinterpret_cast<const float4*>(part ? a.o2 : a.o1);
-    for (int w0 = warp; w0 < nw; w0 += 32 * W) {
-      const int w = w0 + lane * W, cta = c_lo + w / split, i = w % split;
-      float2 v = make_float2(-INFINITY, 0.f);
-      int64_t at = 0;
-      if (w < nw) {
-        const PdRange rg = a.ranges[cta];
-        int lo = part ? rg.s0 : rg.p0, hi = part ? rg.s1 : rg.p1;
-        if (split == 2) {
-          const int mid = part ? rg.sm : rg.pm;
-          if (i == 0) hi = mid; else lo = mid;
-        }
-        at = ((int64_t)split * cta + i + u) * per + row;
-        if (max((int64_t)lo, first) < min((int64_t)hi, first + n)) v = __ldcg(ml + at);
+  const float4* o1 = reinterpret_cast<const float4*>(a.o1);
+  const float4* o2 = reinterpret_cast<const float4*>(a.o2);
+  for (int w0 = warp; w0 < p[0].nw + p[1].nw; w0 += 32 * W) {
+    int w = w0 + lane * W;
+    const bool own = w >= p[0].nw;
+    const Part q = own ? p[1] : p[0];
+    if (own) w -= p[0].nw;
+    float2 v = make_float2(-INFINITY, 0.f);
+    const float4* src = o1;
+    if (w < q.nw) {
+      const int cta = q.c_lo + w / q.split, i = w % q.split;
+      const PdRange rg = a.ranges[cta];
+      int lo = own ? rg.s0 : rg.p0, hi = own ? rg.s1 : rg.p1;
+      if (q.split == 2) {
+        const int mid = own ? rg.sm : rg.pm;
+        if (i == 0) hi = mid; else lo = mid;
       }
-      const float top = fmaxf(M, warp_max(v.x));
-      if (top == -INFINITY) continue;
-      const float keep = M == -INFINITY ? 0.f : ex2(M - top);
-      const float f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
-      M = top;
-      Ls = Ls * keep + warp_sum(v.y * f);
-      A.x *= keep;
-      A.y *= keep;
-      A.z *= keep;
-      A.w *= keep;
-      unsigned todo = __ballot_sync(0xffffffffu, f != 0.f);
-      while (todo) {
-        float4 x[4];
-        float fs[4];
+      const int64_t at = ((int64_t)q.split * cta + i + q.u) * q.per + q.row;
+      src = (own ? o2 : o1) + at * (kHeadDim / 4);
+      if (max((int64_t)lo, q.first) < min((int64_t)hi, q.first + q.n))
+        v = __ldcg((own ? a.ml2 : a.ml1) + at);
+    }
+    const float top = fmaxf(M, warp_max(v.x));
+    if (top == -INFINITY) continue;
+    const float keep = M == -INFINITY ? 0.f : ex2(M - top);
+    const float f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
+    M = top;
+    Ls = Ls * keep + warp_sum(v.y * f);
+    A.x *= keep;
+    A.y *= keep;
+    A.z *= keep;
+    A.w *= keep;
+    unsigned todo = __ballot_sync(0xffffffffu, f != 0.f);
+    while (todo) {
+      float4 x[4];
+      float fs[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int src = todo ? __ffs(todo) - 1 : 0;
-          fs[j] = __shfl_sync(0xffffffffu, f, src);
-          const int64_t as = __shfl_sync(0xffffffffu, at, src);
-          if (!todo) fs[j] = 0.f;
-          x[j] = todo ? __ldcg(o + as * (kHeadDim / 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-          todo &= todo - 1;
-        }
+      for (int j = 0; j < 4; ++j) {
+        const int from = todo ? __ffs(todo) - 1 : 0;
+        fs[j] = __shfl_sync(0xffffffffu, f, from);
+        const float4* s = reinterpret_cast<const float4*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), from));
+        if (!todo) fs[j] = 0.f;
+        x[j] = todo ? __ldcg(s + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        todo &= todo - 1;
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          A.x = __fmaf_rn(fs[j], x[j].x, A.x);
-          A.y = __fmaf_rn(fs[j], x[j].y, A.y);
-          A.z = __fmaf_rn(fs[j], x[j].z, A.z);
-          A.w = __fmaf_rn(fs[j], x[j].w, A.w);
-        }
+      for (int j = 0; j < 4; ++j) {
+        A.x = __fmaf_rn(fs[j], x[j].x, A.x);
+        A.y = __fmaf_rn(fs[j], x[j].y, A.y);
+        A.z = __fmaf_rn(fs[j], x[j].z, A.z);
+        A.w = __fmaf_rn(fs[j], x[j].w, A.w);
       }
     }
   }
@@ -774,9 +867,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
     }
   }
   const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-  const __half2 o2[2] = {__floats2half2_rn(A.x * inv, A.y * inv),
-                         __floats2half2_rn(A.z * inv, A.w * inv)};
-  *reinterpret_cast<uint2*>(a.out + bh * kHeadDim + 4 * lane) = *reinterpret_cast<const uint2*>(o2);
+  const __half2 r[2] = {__floats2half2_rn(A.x * inv, A.y * inv),
+                        __floats2half2_rn(A.z * inv, A.w * inv)};
+  *reinterpret_cast<uint2*>(a.out + bh * kHeadDim + 4 * lane) = *reinterpret_cast<const uint2*>(r);
   if (a.lse && lane == 0)
     a.lse[bh] = Ls > 0.f ? (M + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
 }
@@ -803,7 +896,7 @@ static PdPlan pd_plan(int B, int Hq, int Hk, int P) {
   p.ranges = at;
   at += up(kPdCtas * sizeof(PdRange));
   p.cum = at;
-  at += up(((size_t)B + 1) * sizeof(int));
+  at += up(((size_t)B + 1) * sizeof(uint64_t));
   p.ml1 = at;
   at += up(slots1 * p.rows1 * sizeof(float2));
   p.o1 = at;
@@ -883,7 +976,7 @@ cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int p
   a.ml1 = reinterpret_cast<float2*>(w + p.ml1);
   a.o2 = reinterpret_cast<float*>(w + p.o2);
   a.ml2 = reinterpret_cast<float2*>(w + p.ml2);
-  a.cum = reinterpret_cast<int*>(w + p.cum);
+  a.cum = reinterpret_cast<uint64_t*>(w + p.cum);
   a.ranges = reinterpret_cast<PdRange*>(w + p.ranges);
   a.status = reinterpret_cast<int*>(w);
   a.out = out;
@@ -906,7 +999,7 @@ cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int p
     e = launch_k(k_prefix_decode, dim3(kPdCtas), dim3(kPdThreads), kPdSmem, st, false, mk, mv, mq, mq1,
                  a);
     if (e != cudaSuccess) return e;
-  } else if ((e = cudaMemsetAsync(a.cum, 0, ((size_t)L.B + 1) * sizeof(int), st)) != cudaSuccess) {
+  } else if ((e = cudaMemsetAsync(a.cum, 0, ((size_t)L.B + 1) * sizeof(uint64_t), st)) != cudaSuccess) {
     return e;
   }
   // records of a row of the prefix: the CTAs that share its unit, two streams each
