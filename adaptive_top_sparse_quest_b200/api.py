@@ -598,18 +598,24 @@ def _need_on(t: torch.Tensor, dtype, name: str, device, shape=None):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+# The current stream's handle without a Stream object (3 us of a call's 10).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(f, where: str, device: torch.device, stream, *args) -> None:
     """f(*args, stream) with the tensors' device current; `stream`, or that
     device's current stream."""
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        st = torch.cuda.current_stream() if stream is None else stream
-        check(f(*args, st.cuda_stream), where)
+        status = f(*args, handle)
     else:
         with torch.cuda.device(device):
-            st = torch.cuda.current_stream() if stream is None else stream
-            check(f(*args, st.cuda_stream), where)
+            status = f(*args, handle)
+    if status:
+        check(status, where)
 
 
 class PageTableUpdate:
@@ -676,15 +682,18 @@ def update_page_table(seq_lens: torch.Tensor, new_lens: torch.Tensor, page_table
 def _token_rows(t: torch.Tensor, name: str, kv: KVCache, T: int) -> int:
     """Check new rows [T][Hk][128] (a slice of a wider projection may be given:
     only the last two dimensions must be packed).  Returns the token stride."""
-    if t.dtype != torch.float16 or t.device != kv.k.device or t.shape != (T, kv.Hk, HEAD_DIM):
-        raise ValueError(f"{name} must be fp16 [{T}][{kv.Hk}][128] on {kv.k.device}")
-    st, sh, sd = t.stride()
-    if sd != 1 or (kv.Hk > 1 and sh != HEAD_DIM):
+    Hk = kv.k.shape[1]
+    if t.dtype is not torch.float16 or t.device != kv.k.device or t.shape != (T, Hk, HEAD_DIM):
+        raise ValueError(f"{name} must be fp16 [{T}][{Hk}][128] on {kv.k.device}")
+    stride, sh, sd = t.stride()
+    if sd != 1 or (sh != HEAD_DIM and Hk > 1):
         raise ValueError(f"{name}: a token's heads must lie side by side")
-    stride = st if T > 1 else kv.Hk * HEAD_DIM
-    if stride < kv.Hk * HEAD_DIM or stride % 8:
+    width = Hk * HEAD_DIM
+    if T <= 1:
+        return width
+    if stride < width or stride % 8:
         raise ValueError(f"{name}: token stride {stride} must be a multiple of 8, "
-                         f"at least {kv.Hk * HEAD_DIM}")
+                         f"at least {width}")
     return stride
 
 
@@ -695,28 +704,31 @@ def write_rows(kv: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: tor
     skips) and, in the same pass, quantise the keys into `keys` and fold them
     into `meta` (if given): tw_write_rows."""
     lib = _capi.load()
-    dev = kv.k.device
+    k = kv.k
+    dev = k.device
     if kv.v is None:
         raise ValueError("the cache has no v")
-    _need_on(slots, torch.int32, "slots", dev)
     if slots.dim() != 1:
         raise ValueError("slots must be [T]")
-    T = int(slots.shape[0])
+    if slots.dtype is not torch.int32 or slots.device != dev or not slots.is_contiguous():
+        _need_on(slots, torch.int32, "slots", dev)
+    T = slots.shape[0]
     ks, vs = _token_rows(k_new, "k_new", kv, T), _token_rows(v_new, "v_new", kv, T)
+    codes = scales = zeros = None
     if keys is not None:
-        _need_on(keys.codes, torch.uint8, "codes", dev)
+        codes, scales, zeros = keys.codes, keys.scales, keys.zeros
         _check_keys(kv, keys)
-        _need_on(keys.scales, torch.float16, "scales", dev, kv.row_shape(4))
-        _need_on(keys.zeros, torch.float16, "zeros", dev, kv.row_shape(4))
+        _need_on(codes, torch.uint8, "codes", dev)
+        groups = kv.row_shape(4)
+        _need_on(scales, torch.float16, "scales", dev, groups)
+        _need_on(zeros, torch.float16, "zeros", dev, groups)
     if meta is not None:
         _need_on(meta, torch.float16, "meta", dev, kv.meta_shape())
     if T == 0:
         return
-    s = kv.struct()
     _launch(lib.tw_write_rows, "tw_write_rows", dev, stream,
-            ctypes.byref(s), _ptr(k_new), ks, _ptr(v_new), vs, _ptr(slots), T,
-            _ptr(keys.codes) if keys else None, _ptr(keys.scales) if keys else None,
-            _ptr(keys.zeros) if keys else None, _ptr(meta))
+            ctypes.byref(kv.struct()), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+            slots.data_ptr(), T, _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(meta))
 
 
 def prefix_workspace_bytes(B: int, Hq: int, Hk: int, prefix_len: int) -> int:
