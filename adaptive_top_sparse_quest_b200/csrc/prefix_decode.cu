@@ -255,6 +255,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     mbar_init(&c.drain, 2);
     mbar_fence_init();
   }
+  griddep_wait();   // what follows reads and writes memory
   // own key tiles of all sequences, this CTA's stretch of the line of costs, and
   // the tiles at its ends and its middle
   {
@@ -743,10 +744,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
   __shared__ float4 acc_s[kJoinWarps][32];
   __shared__ float2 ml_s[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W;
-  const int64_t bh = (int64_t)blockIdx.x * (kJoinWarps / W) + (threadIdx.x >> 5) / W;
+  const int bh = (int)blockIdx.x * (kJoinWarps / W) + (threadIdx.x >> 5) / W;   // output row
+  const int lgG = 31 - __clz(a.G);   // G is a power of two
+  const int b = bh / a.Hq, hq = bh - b * a.Hq, h = hq >> lgG, g = hq & (a.G - 1);
   griddep_wait();
-  if (W < kJoinWarps && bh >= (int64_t)a.L.B * a.Hq) return;
-  const int b = (int)(bh / a.Hq), hq = (int)(bh % a.Hq), h = hq / a.G, g = hq % a.G;
+  griddep_launch();   // the next call's tile kernel may set itself up
+  if (W < kJoinWarps && bh >= a.L.B * a.Hq) return;
   const int len = a.L.len(b);
   const uint64_t total = __ldcg(a.cum + a.L.B), c0 = __ldcg(a.cum + b), c1 = __ldcg(a.cum + b + 1);
   const int64_t X1 = prefix_span(a), X = X1 + own_cost(total) * a.L.Hk;
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
     float2 v = make_float2(-INFINITY, 0.f);
     const float4* src = o1;
     if (w < q.nw) {
-      const int cta = q.c_lo + w / q.split, i = w % q.split;
+      const int cta = q.c_lo + (w >> (q.split - 1)), i = w & (q.split - 1);
       const PdRange rg = a.ranges[cta];
       int lo = own ? rg.s0 : rg.p0, hi = own ? rg.s1 : rg.p1;
       if (q.split == 2) {
@@ -869,7 +872,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
   const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
   const __half2 r[2] = {__floats2half2_rn(A.x * inv, A.y * inv),
                         __floats2half2_rn(A.z * inv, A.w * inv)};
-  *reinterpret_cast<uint2*>(a.out + bh * kHeadDim + 4 * lane) = *reinterpret_cast<const uint2*>(r);
+  *reinterpret_cast<uint2*>(a.out + (int64_t)bh * kHeadDim + 4 * lane) = *reinterpret_cast<const uint2*>(r);
   if (a.lse && lane == 0)
     a.lse[bh] = Ls > 0.f ? (M + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
 }
@@ -996,7 +999,7 @@ cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int p
                                   (int)kPdSmem);
     });
     if (e != cudaSuccess) return e;
-    e = launch_k(k_prefix_decode, dim3(kPdCtas), dim3(kPdThreads), kPdSmem, st, false, mk, mv, mq, mq1,
+    e = launch_k(k_prefix_decode, dim3(kPdCtas), dim3(kPdThreads), kPdSmem, st, true, mk, mv, mq, mq1,
                  a);
     if (e != cudaSuccess) return e;
   } else if ((e = cudaMemsetAsync(a.cum, 0, ((size_t)L.B + 1) * sizeof(uint64_t), st)) != cudaSuccess) {
