@@ -25,26 +25,27 @@ __device__ __forceinline__ uint32_t h_key2(uint32_t w) {
 }
 
 // Quantise one token row held by a half-warp (lane l16 holds channels
-// 8 l16 .. 8 l16 + 7 in `raw`) to BITS-bit codes (levels 0 .. 2^BITS - 1) and
-// store its codes, scales and zeros at `row`.  Every value is a fixed sequence
-// of IEEE round-to-nearest operations, so it is bit-exact with the CPU
-// definition.  Code j of the lane sits at bits BITS * j of its 4 (BITS = 4) or
-// 2 (BITS = 2) bytes: channel c at bits BITS * (c % (8 / BITS)) of byte
-// c / (8 / BITS).
+// 8 l16 .. 8 l16 + 7 in `raw`, their keys (h_key2) in `key`) to BITS-bit codes
+// (levels 0 .. 2^BITS - 1) and store its codes, scales and zeros at `row`.  Every
+// value equals a fixed sequence of IEEE round-to-nearest operations, so it is
+// bit-exact with the CPU definition.  Code j of the lane sits at bits BITS * j of
+// its 4 (BITS = 4) or 2 (BITS = 2) bytes: channel c at bits BITS * (c % (8 / BITS))
+// of byte c / (8 / BITS).
 template <int BITS>
-__device__ __forceinline__ void quantize_row(const uint4 raw, int64_t row, int lane,
-                                             unsigned hmask, uint8_t* __restrict__ codes,
+__device__ __forceinline__ void quantize_row(const uint4 raw, const uint32_t (&key)[4], int64_t row,
+                                             int lane, unsigned hmask,
+                                             uint8_t* __restrict__ codes,
                                              __half* __restrict__ scales,
                                              __half* __restrict__ zeros) {
   static_assert(BITS == 4 || BITS == 2, "key-cache width");
   constexpr int kLevels = (1 << BITS) - 1;
   const int l16 = lane & 15;
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t lo = h_key2(w[0]), hi = lo;
+  uint32_t lo = key[0], hi = lo;
 #pragma unroll
   for (int j = 1; j < 4; ++j) {
-    lo = __vmins2(lo, h_key2(w[j]));
-    hi = __vmaxs2(hi, h_key2(w[j]));
+    lo = __vmins2(lo, key[j]);
+    hi = __vmaxs2(hi, key[j]);
   }
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
@@ -59,30 +60,39 @@ __device__ __forceinline__ void quantize_row(const uint4 raw, int64_t row, int l
   const float s32 = __fdiv_rn(__fsub_rn(mxf, mnf), (float)kLevels);
   const __half sc = __float2half_rn(s32);
   const float scf = __half2float(sc);
-  // code = rint(fl((x - mn) / scale)).  The product y with the approximate
-  // reciprocal (off by 2^-23 of itself at most) is within 2^-22 of the rounded
-  // quotient, relative; quotients are below 32 (the levels, or 1.5 times as many
-  // where the scale is of fp16's smallest values and rounded down), so within
-  // 2^-17.  Only a y that is about that near to a half-integer can round to
-  // another code: those divide.
+  // code = min(rint(fl((x - mn) / scale)), levels).  The product y with the
+  // approximate reciprocal (off by 2^-23 of itself at most) is within 2^-22 of the
+  // rounded quotient, relative; quotients are below 32 (the levels, or 1.5 times
+  // as many where the scale is of fp16's smallest values and rounded down), so
+  // within 2^-17.  Only a y that is about that near to a half-integer can round to
+  // another code: such a row's lane divides.
+  // 1.5 * 2^23 + y rounds y to the nearest integer, ties to even, into its low
+  // bits; the sum of those bits' shifts, less that of the constants, packs them.
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scf));
   if (scf == 0.0f) inv = 0.0f;   // all codes 0
-  uint32_t packed = 0;
+  constexpr float kBig = 12582912.0f;
+  uint32_t packed = 0, shifts = 0;
+  float d[8];
+  bool near_half = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float x =
-        __half2float(__ushort_as_half((unsigned short)((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu)));
-    const float d = __fsub_rn(x, mnf);
-    // 1.5 * 2^23 + y rounds y to the nearest integer, ties to even, in its low bits
-    float y = __fmul_rn(d, inv), z = __fadd_rn(y, 12582912.0f);
-    if (fabsf(__fsub_rn(y, __fsub_rn(z, 12582912.0f))) > 0.5f - 0x1p-15f) {
-      y = __fdiv_rn(d, scf);
-      z = __fadd_rn(y, 12582912.0f);
-    }
-    const uint32_t c = min(__float_as_uint(z) - 0x4B400000u, (uint32_t)kLevels);
-    packed |= c << (BITS * j);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j >> 1]));
+    d[j] = __fsub_rn(j & 1 ? x.y : x.x, mnf);
+    const float y = fminf(__fmul_rn(d[j], inv), (float)kLevels), z = __fadd_rn(y, kBig);
+    near_half |= fabsf(__fsub_rn(y, __fsub_rn(z, kBig))) > 0.5f - 0x1p-15f;
+    packed += __float_as_uint(z) * (1u << (BITS * j));
+    shifts += 0x4B400000u * (1u << (BITS * j));
   }
+  if (near_half) {
+    packed = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float y = scf == 0.0f ? 0.0f : fminf(__fdiv_rn(d[j], scf), (float)kLevels);
+      packed += __float_as_uint(__fadd_rn(y, kBig)) * (1u << (BITS * j));
+    }
+  }
+  packed -= shifts;
   if (BITS == 4)
     *reinterpret_cast<uint32_t*>(codes + row * (kHeadDim / 2) + l16 * 4) = packed;
   else
@@ -121,8 +131,9 @@ k_quantize_keys(Layout L, const __half* __restrict__ K, uint8_t* __restrict__ co
     const int b = (int)(bh / L.Hk);
     if (t >= L.len(b)) continue;  // uniform across the half-warp
     const int64_t row = L.row(b, h, t);
-    quantize_row<BITS>(ld_stream16(K + row * kHeadDim + l16 * 8), row, lane, hmask, codes,
-                       scales, zeros);
+    const uint4 raw = ld_stream16(K + row * kHeadDim + l16 * 8);
+    const uint32_t key[4] = {h_key2(raw.x), h_key2(raw.y), h_key2(raw.z), h_key2(raw.w)};
+    quantize_row<BITS>(raw, key, row, lane, hmask, codes, scales, zeros);
   }
 }
 
@@ -150,7 +161,10 @@ k_append_keys(Layout L, const __half* __restrict__ K, uint8_t* __restrict__ code
     if (t < 0) continue;  // uniform across the half-warp
     const int64_t row = L.row(b, h, t);
     const uint4 raw = *reinterpret_cast<const uint4*>(K + row * kHeadDim + l16 * 8);
-    if (codes) quantize_row<BITS>(raw, row, lane, hmask, codes, scales, zeros);
+    if (codes) {
+      const uint32_t key[4] = {h_key2(raw.x), h_key2(raw.y), h_key2(raw.z), h_key2(raw.w)};
+      quantize_row<BITS>(raw, key, row, lane, hmask, codes, scales, zeros);
+    }
     if (meta) {
       __half* dst = meta + L.meta_index(b, h, t / kPage) * (2 * kHeadDim) + l16 * 8;
       const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -278,12 +292,13 @@ k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restric
           const int64_t at = row + c + 2 * x;
           *reinterpret_cast<uint4*>(K + at * kHeadDim + l16 * 8) = kr[x];
           *reinterpret_cast<uint4*>(V + at * kHeadDim + l16 * 8) = vr[x];
-          if (codes) quantize_row<BITS>(kr[x], at, lane, hmask, codes, scales, zeros);
-          const uint32_t w[4] = {kr[x].x, kr[x].y, kr[x].z, kr[x].w};
+          const uint32_t key[4] = {h_key2(kr[x].x), h_key2(kr[x].y), h_key2(kr[x].z),
+                                   h_key2(kr[x].w)};
+          if (codes) quantize_row<BITS>(kr[x], key, at, lane, hmask, codes, scales, zeros);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            kmin[j] = __vmins2(kmin[j], h_key2(w[j]));
-            kmax[j] = __vmaxs2(kmax[j], h_key2(w[j]));
+            kmin[j] = __vmins2(kmin[j], key[j]);
+            kmax[j] = __vmaxs2(kmax[j], key[j]);
           }
         }
     }
@@ -396,9 +411,10 @@ cudaError_t launch_write_rows(const Layout& L, const __half* k_new, const __half
                               __half* K, __half* V, uint8_t* codes, __half* scales, __half* zeros,
                               __half* meta, cudaStream_t st, int num_sms) {
   // list places per block: as many as a page has rows, fewer while the grid
-  // would not give every SM two blocks (single tokens are a run each)
+  // would not give every SM four blocks (single tokens are a run each; of a
+  // prompt's places only every 16th starts a run)
   int chunk = kWrMaxChunk;
-  while (chunk > 1 && (T + chunk - 1) / chunk < 2 * num_sms) chunk /= 2;
+  while (chunk > 1 && (T + chunk - 1) / chunk < 4 * num_sms) chunk /= 2;
   const dim3 grid((T + chunk - 1) / chunk, (L.Hk + kWrHeads - 1) / kWrHeads);
   return launch_k(L.kbits == 2 ? k_write_rows<2> : k_write_rows<4>, grid, dim3(kWrThreads), 0, st,
                   false, L, k_new, v_new, k_stride, v_stride, slots, T, chunk, K, V, codes, scales,
