@@ -706,8 +706,10 @@ def write_rows(kv: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: tor
     lib = _capi.load()
     k = kv.k
     dev = k.device
-    if kv.v is None:
-        raise ValueError("the cache has no v")
+    if kv.v is None or kv.v.device != dev:
+        raise ValueError(f"the cache needs a v on {dev}")
+    if not kv.paged and k.shape[0] < kv.B:
+        raise ValueError(f"the cache has {k.shape[0]} sequences, seq_lens {kv.B}")
     if slots.dim() != 1:
         raise ValueError("slots must be [T]")
     if slots.dtype is not torch.int32 or slots.device != dev or not slots.is_contiguous():

@@ -9,24 +9,37 @@
 // so the shared part is read once per 256 query rows instead of once per
 // sequence; a sequence's own tokens meet its G rows the same way.  A softmax
 // over any subset of the keys is summed up by (m, l = sum P, O); subsets are
-// joined by weights 2^(m_i - m).  Each CTA takes an equal share of all key
-// tiles (128 keys), writes a record (m, l, O) per row and unit it touched, and
-// a second kernel joins a row's records.
+// joined by weights 2^(m_i - m).  Each CTA takes an equal share of the key tiles
+// (128 keys), writes a record (m, l, O) per row and unit it touched, and a second
+// kernel joins a row's records.
 //
-// Pipeline.  One CTA per SM, twelve warps, two independent streams of tiles:
-//   - a producer warp per stream copies K and V (page by page, 16 rows x 64
-//     columns per tensor-map copy, 128-byte swizzle) into its 64 KB of buffers;
+// Pipeline.  One CTA per SM, twelve warps, two streams of tiles:
+//   - a warp per stream copies its query rows, and K and V (page by page, 16 rows
+//     x 64 columns per tensor-map copy, 128-byte swizzle) into 64 KB of buffers;
 //   - a warp per stream issues tcgen05: S (128 x 128, fp32) into tensor memory,
 //     and O += P V with P read from tensor memory, where it overwrites S;
-//   - four warps per stream hold one query row per thread: they read S, keep
-//     the running maximum and sum in registers, and write P.  O is rescaled
-//     only when a row's maximum has risen by more than 2^8 (its weights still
-//     fit fp16: they are scaled to at most 2^15, so that what falls below
-//     fp16's normal range is below 2^-21 of the row's largest at least).
-// While one stream's softmax runs, the other's products do.  With more than
-// 128 query rows per KV head the two streams are two row tiles on the same K / V
-// buffers, which halves the traffic; with fewer they take separate tiles of
-// keys.  Tensor memory: S0 | S1 | O0 | O1, 128 columns each.
+//   - four warps per stream hold one query row per thread: they read S twice (the
+//     maximum, then the weights), and write P, the first half ahead of the second.
+//     The running maximum and sum stay in registers, in fp32.  P is rounded to
+//     fp16, as the products need it: 2^-11 of each weight.  O is rescaled only
+//     when a row's maximum has risen by more than 2^8: the weights are lifted to
+//     between 2^7 and 2^15 at the maximum, so that they fit fp16, and what falls
+//     below its normal range is below 2^-21 of the row's largest.
+// With more than 128 query rows per KV head the two streams are two row tiles on
+// the same K / V buffers, which halves the traffic, and one stream's softmax runs
+// while the other's products do; with fewer they take separate tiles of keys.
+// Tensor memory: S0 | S1 | O0 | O1, 128 columns each.
+//
+// What bounds it (one B200; both kernels, sustained, in us):
+//   - few query rows (16 sequences of 1000 .. 9000 tokens, nothing shared): HBM;
+//     the tile kernel reads 307 MB in 54, 0.87 of the measured copy rate, and the
+//     call takes 63 with its start, the join and the gap between the two;
+//   - 512 rows per head (128 sequences behind 128k tokens): power.  A tile of 256
+//     rows takes 2930 clocks, 2048 of them tensor-core time, and the clock falls
+//     to 1.3 GHz at the 1000 W cap: 340, 0.81 PFLOP/s; started cold 250;
+//   - 256 rows (64 behind 32k): both, and the 19 MB of records written and read;
+//   - small calls: latency: set-up 2, first copies 2, a tile's chain 2, the
+//     records and the join 6.
 #include <cstring>
 
 #include "tw_common.cuh"
@@ -45,10 +58,11 @@ constexpr float kPdScale = 1.4426950408889634f * 0.08838834764831845f;   // log2
 constexpr float kLift = 7.f;                    // weights are 2^(s - m + 7), m within 2^8 of the maximum
 constexpr float kSlack = 8.f;
 
-// 2^x of two values by arithmetic, for some of the weights: the special-function
-// unit's 16 exponentials per clock and SM are what bounds the softmax (128 x 128
-// weights take it the 1024 clocks that the tile's two products take the tensor
-// cores).  x = n + f with n the nearest integer, f in [-1/2, 1/2] and 2^f by a
+// 2^x of two values by arithmetic, for a quarter of the weights: the special-
+// function unit gives 16 exponentials per clock and SM, so that 128 x 128 weights
+// take it the 1024 clocks that the tile's two products take the tensor cores
+// (64 sequences behind 128k tokens: 129 us; 138 with none by arithmetic, 132 with
+// half).  x = n + f with n the nearest integer, f in [-1/2, 1/2] and 2^f by a
 // polynomial of degree 4 fitted to the least relative error, 2.6e-6: a 200th of
 // the rounding to fp16 that follows.  Below 2^-125 the result is 2^-125.
 __device__ __forceinline__ float2 ex2_poly(uint64_t x) {
@@ -100,7 +114,10 @@ struct PdArgs {
 };
 
 struct PdCtl {
-  uint64_t kfull[2], vfull[2], kempty[2], vempty[2], qfull[2], qempty[2], sfull[2], pfull[2], phalf[2], ofull[2], shared_done, drain;
+  uint64_t kfull[2], vfull[2], kempty[2], vempty[2];   // per buffer set
+  uint64_t qfull[2], qempty[2];                        // per stream: query rows,
+  uint64_t sfull[2], phalf[2], pfull[2], ofull[2];     // S, P's first half, P, a segment's O
+  uint64_t shared_done, drain;
   uint32_t tmem;
   uint64_t red[kPdThreads / 32];
   PdRange range;
@@ -751,7 +768,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
   griddep_launch();   // the next call's tile kernel may set itself up
   if (W < kJoinWarps && bh >= a.L.B * a.Hq) return;
   const int len = a.L.len(b);
-  const uint64_t total = __ldcg(a.cum + a.L.B), c0 = __ldcg(a.cum + b), c1 = __ldcg(a.cum + b + 1);
+  // (through L1: every row's warps read the same few words)
+  const uint64_t total = a.cum[a.L.B], c0 = a.cum[b], c1 = a.cum[b + 1];
   const int64_t X1 = prefix_span(a), X = X1 + own_cost(total) * a.L.Hk;
   // what lies at x is CTA floor(x kPdCtas / X)'s or, after rounding, a
   // neighbour's; the CTAs' own ranges decide
