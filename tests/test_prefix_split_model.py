@@ -132,13 +132,14 @@ def check(Hk, RT, KT, pair, kts):
 def test_every_tile_once_and_every_record_found(seed):
     rng = random.Random(seed)
     for _ in range(12):
-        Hk, RT = rng.choice([1, 2, 8, 32]), rng.choice([1, 1, 2, 4])
+        Hk, pair = rng.choice([1, 2, 8, 32]), rng.random() < 0.5
+        RT = rng.choice([1, 1, 2, 4]) if pair else 1   # row tiles of 256; one below 128 rows
         KT = rng.choice([0, 0, 1, 2, 5, 32, 256, 1024])
         B = rng.choice([1, 2, 5, 30])
         top = rng.choice([1, 3, 10, 100])
         kts = [rng.choice([0, rng.randint(0, top), rng.randint(0, top)]) for _ in range(B)]
         if Hk * RT * KT + sum(kts):
-            check(Hk, RT, KT, rng.random() < 0.5, kts)
+            check(Hk, RT, KT, pair, kts)
 
 
 def test_one_tile_and_one_long_sequence():
