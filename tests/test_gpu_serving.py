@@ -403,6 +403,153 @@ def test_prefix_decode_refusals():
         step(q.float())
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_prefix_decode_random_shapes(seed):
+    """Shapes drawn over the whole range: heads, batch, prefix, ragged own parts."""
+    rng = random.Random(100 + seed)
+    G, Hk = rng.choice([1, 2, 4, 8]), rng.choice([1, 2, 3, 8])
+    B = rng.choice([1, 2, 7, 16, 33, 65, 130])
+    P = 16 * rng.choice([0, 1, 7, 8, 9, 40, 130])
+    top = rng.choice([1, 20, 130, 600])
+    lens = [rng.choice([P + rng.randint(0, top), P + rng.randint(0, top), rng.randint(0, P)])
+            for _ in range(B)]
+    c = dict(Hq=G * Hk, Hk=Hk, P=P, lens=lens, paged=rng.random() < 0.6)
+    step, (q, k, v, table, lens) = _run_prefix(c, seed=seed)
+    step(q)
+    _check_status(step)
+    check_attention(q, k, v, table, lens.tolist(), step.out, step.lse)
+
+
+def test_prefix_decode_many_row_tiles():
+    """2048 query rows per KV head: eight row tiles of 256."""
+    c = dict(Hq=64, Hk=8, P=528, lens=[528 + (i * 7) % 40 for i in range(256)], paged=True)
+    step, (q, k, v, table, lens) = _run_prefix(c)
+    step(q)
+    _check_status(step)
+    check_attention(q, k, v, table, lens.tolist(), step.out, step.lse)
+
+
+def test_prefix_decode_back_to_back_with_changing_inputs():
+    """Calls without a wait between them, queries and lengths written by kernels
+    of the same stream just before each: every call sees its own inputs."""
+    c = dict(Hq=8, Hk=2, P=128, lens=[704, 512, 304, 128, 256, 640], paged=True)
+    step, (q, k, v, table, lens) = _run_prefix(c)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    qs = torch.randn(40, *q.shape, generator=g, device="cuda", dtype=torch.float16)
+    full = torch.tensor(c["lens"], device="cuda")
+    all_lens = (full * torch.rand(40, len(full), generator=g, device="cuda")).to(torch.int32)
+    x, a = torch.empty_like(q), torch.randn(512, 512, device="cuda", dtype=torch.float16)
+    outs, lses = [], []
+    for i in range(40):
+        if i % 3 == 1:
+            a = a @ a * 1e-2              # a library product between two calls
+        x.copy_(qs[i])
+        lens.copy_(all_lens[i])
+        step(x)
+        outs.append(step.out.clone())
+        lses.append(step.lse.clone())
+    torch.cuda.synchronize()
+    _check_status(step)
+    # rows past a shorter length hold other rows, not NaN: the reference takes the length
+    for i in range(0, 40, 3):
+        check_attention(qs[i], k, v, table, all_lens[i].tolist(), outs[i], lses[i])
+
+
+def test_prefix_decode_hostile_table_and_lengths():
+    """Lengths outside [0, N] are clamped; page ids outside the pool read some
+    page of it, which spoils that sequence and no other."""
+    from adaptive_top_sparse_quest_b200 import KVCache, PrefixDecodeStep
+    q, k, v, table, lens = make_prefix_case(6, 8, 2, 32, [100, 90, 112, 64], True)
+    k.nan_to_num_()
+    v.nan_to_num_()
+    table[1, 3] = -7
+    table[1, 5] = 2 ** 31 - 1
+    bad = i32([100, 90, 2 ** 31 - 1, -5])
+    step = PrefixDecodeStep(KVCache(k, v, bad, table), 8, 32)
+    step(q)
+    _check_status(step)
+    N = table.shape[1] * PAGE
+    assert bool(torch.isfinite(step.out).all())
+    good = [0, 2, 3]
+    check_attention(q[good], k, v, table[good], [100, N, 0], step.out[good], step.lse[good])
+
+
+def test_long_pool_offsets():
+    """Rows past 2^31 elements of the pool: written by slot, quantised, attended to."""
+    from adaptive_top_sparse_quest_b200 import KVCache, PrefixDecodeStep, write_rows
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    Hk, pool, W = 32, 40000, 6
+    k = torch.empty(pool, Hk, PAGE, D, dtype=torch.float16, device="cuda")
+    v = torch.empty_like(k)
+    table = i32([[pool - 1 - j for j in range(W)], [pool - 50 - 3 * j for j in range(W)]])
+    lens = i32([90, 77])
+    kv = KVCache(k, v, lens, table)
+    slots = i32([int(table[b, t // PAGE]) * PAGE + t % PAGE
+                 for b, n in enumerate((90, 77)) for t in range(n)])
+    g = torch.Generator(device="cuda").manual_seed(2)
+    new = torch.randn(2, 167, Hk, D, generator=g, device="cuda", dtype=torch.float16)
+    meta = torch.empty(kv.meta_shape(), dtype=torch.float16, device="cuda")
+    write_rows(kv, new[0], new[1], slots, None, meta)
+    s = slots.long()
+    assert torch.equal(k[s // PAGE, :, s % PAGE], new[0])
+    assert torch.equal(v[s // PAGE, :, s % PAGE], new[1])
+    want = k[pool - 1].amin(1), k[pool - 1].amax(1)
+    assert torch.equal(meta[pool - 1, :, 0], want[0]) and torch.equal(meta[pool - 1, :, 1], want[1])
+    q = torch.randn(2, Hk, D, generator=g, device="cuda", dtype=torch.float16)
+    step = PrefixDecodeStep(kv, Hk, 0)
+    step(q)
+    _check_status(step)
+    check_attention(q, k, v, table, [90, 77], step.out, step.lse)
+
+
+def test_write_rows_captured_and_slot_listed_twice():
+    """A captured write replayed with other rows and slots; a slot that is listed
+    twice holds one of its rows, and nothing else changes."""
+    from adaptive_top_sparse_quest_b200 import write_rows
+    kv = _cache(2, 2, 4, True, 0, 4)
+    new = torch.randn(4, 2, D, device="cuda").half()
+    slots = i32([-1, -1, -1, -1])
+    write_rows(kv, new, new, slots)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        write_rows(kv, new, new, slots)
+    want = kv.k.clone()
+    for s in ([17, 18, 40, -1], [33, 3, 4, 5], [-1, 20, 20, -1]):
+        new.copy_(torch.randn(4, 2, D, device="cuda"))
+        slots.copy_(i32(s))
+        g.replay()
+        for i, x in enumerate(s):
+            if x >= 0:
+                want[x // PAGE, :, x % PAGE] = new[i]
+        if s[1] == s[2]:
+            got = kv.k[1, :, 4]
+            assert all(any(torch.equal(got[h], new[i, h]) for i in (1, 2)) for h in range(2))
+            want[1, :, 4] = got
+        assert torch.equal(kv.k, want)
+
+
+def test_serving_calls_on_a_side_stream():
+    from adaptive_top_sparse_quest_b200 import prefix_decode, update_page_table, write_rows
+    old, new, table, free, nf, ns = _pages_case(31, 20, 10, 0, 60, 0.5)
+    st = torch.cuda.Stream()
+    table_t, free_t, o, n, f = i32(table), i32(free), i32(old), i32(new), i32([nf])
+    kv = _cache(2, 2, 4, True, 0, 4)
+    rows = torch.randn(3, 2, D, device="cuda").half()
+    slots = i32([20, 21, 22])
+    q, k, v, tb, lens = make_prefix_case(8, 8, 2, 32, [50, 32, 0], True)
+    torch.cuda.synchronize()
+    u = update_page_table(o, n, table_t, free_t, f, num_slots=ns, stream=st)
+    write_rows(kv, rows, rows, slots, stream=st)
+    from adaptive_top_sparse_quest_b200 import KVCache
+    out, lse = prefix_decode(q, KVCache(k, v, lens, tb), 32, stream=st)
+    st.synchronize()
+    want = model_page_table(old, new, table, free, nf, ns, 0)
+    assert u.seq_lens_out.tolist() == want[0] and u.slots.tolist() == want[2]
+    assert torch.equal(kv.k[1, :, 4:7], rows.transpose(0, 1))
+    check_attention(q, k, v, tb, lens.tolist(), out, lse)
+
+
 # ------------------------------------------------------------------------------- all together
 def test_serving_loop():
     """Requests come, grow, are refused and finish behind a shared prefix: table
