@@ -57,6 +57,8 @@ constexpr uint32_t kBuf = 2 * kBlk;             // a tile of Q, K or V: 32 KB
 constexpr float kPdScale = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
 constexpr float kLift = 7.f;                    // weights are 2^(s - m + 7), m within 2^8 of the maximum
 constexpr float kSlack = 8.f;
+constexpr int kThin = 8;                        // query rows of a thin segment at most
+constexpr int kThinCols = 16;                   // columns of its products (the least there are)
 
 // 2^x of two values by arithmetic, for a quarter of the weights: the special-
 // function unit gives 16 exponentials per clock and SM, so that 128 x 128 weights
@@ -113,6 +115,13 @@ struct PdArgs {
   float* lse;
 };
 
+// What the four softmax warps of a stream exchange over a thin segment.
+struct PdThin {
+  float x[4][kThin];     // a value per warp and row: maxima, at the end sums
+  float m[kThin];
+  int lim[kThin];        // keys a row sees
+};
+
 struct PdCtl {
   uint64_t kfull[2], vfull[2], kempty[2], vempty[2];   // per buffer set
   uint64_t qfull[2], qempty[2];                        // per stream: query rows,
@@ -122,12 +131,15 @@ struct PdCtl {
   uint64_t red[kPdThreads / 32];
   PdRange range;
   int at_b[2], at_h[2], at_t[2];   // where each stream's own tiles begin
+  PdThin thin[2];
 };
-constexpr uint32_t kPdCtlBytes = 512;
+constexpr uint32_t kPdCtlBytes = 1280;
 static_assert(sizeof(PdCtl) <= kPdCtlBytes, "control block");
-// Q, K, V tiles of both streams | control block | 4 KB per softmax warp to write
-// records through | alignment to 1 KB
-constexpr size_t kPdSmem = 6 * kBuf + kPdCtlBytes + 8 * 4096 + 1024;
+// Q, K, V tiles of both streams | 4 KB per softmax warp to write records through,
+// a thin segment's P at the head of each stream's | control block | alignment to 1 KB
+constexpr uint32_t kStage = 4096;
+constexpr size_t kPdSmem = 6 * kBuf + 8 * kStage + kPdCtlBytes + 1024;
+static_assert(kPdSmem <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ int own_tiles(const PdArgs& a, int b) {
   const int n = a.L.len(b) - a.P;
@@ -235,6 +247,15 @@ __device__ __forceinline__ int seg_rows(const PdArgs& a, const Seg& g, int i) {
   return left < 0 ? 0 : min(left, kTile);
 }
 
+// Segments of at most kThin query rows are turned round: S^T = K Q^T and
+// O^T += V^T P^T, keys and then channels along the tensor cores' 128 rows and the
+// query rows along 16 columns.  A product then costs a quarter or less (it is
+// bound by reading K or V from shared memory, 256 clocks a tile) and the softmax
+// has a key per thread instead of a row of 128 keys.
+__device__ __forceinline__ bool is_thin(const PdArgs& a, const Seg& g) {
+  return !g.prefix || (!a.pair && a.M <= kThin);
+}
+
 // A value that is the same in all lanes, in a form that lets the compiler know:
 // it then keeps operand descriptors in uniform registers.
 __device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -250,7 +271,8 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   auto q_buf = [&](int i) { return base + i * kBuf; };
   auto k_buf = [&](int i) { return base + (2 + i) * kBuf; };
   auto v_buf = [&](int i) { return base + (4 + i) * kBuf; };
-  PdCtl& c = *reinterpret_cast<PdCtl*>(smem + 6 * kBuf);
+  auto p_buf = [&](int i) { return base + 6 * kBuf + 4 * i * kStage; };
+  PdCtl& c = *reinterpret_cast<PdCtl*>(smem + 6 * kBuf + 8 * kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = (int)uni(tid >> 5);
   griddep_launch();   // the joining kernel waits for this grid's end by itself
 
@@ -423,16 +445,32 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     auto issue_s = [&](const int i, uint32_t set, uint32_t np) {   // S = Q K^T
       const uint32_t s_col = tmem + i * kTile;
       const uint64_t qd = umma_desc(q_buf(i), 16, 1024), kd = umma_desc(k_buf(set), 16, 1024);
-      const uint32_t id = umma_idesc(np * kPage, false);
+      const uint32_t id = umma_idesc(np * kPage, false, false);
       umma_ss4(s_col, qd, kd, id, 0);
       umma_ss4(s_col, qd + (kBlk >> 4), kd + (kBlk >> 4), id, 1);
       umma_commit(&c.sfull[i]);
+    };
+    // thin: S^T = K Q^T, O^T += V^T P^T
+    auto issue_s_thin = [&](const int i) {
+      const uint64_t qd = umma_desc(q_buf(i), 16, 1024), kd = umma_desc(k_buf(i), 16, 1024);
+      const uint32_t id = umma_idesc(kThinCols, false, false);
+      umma_ss4(tmem + i * kTile, kd, qd, id, 0);
+      umma_ss4(tmem + i * kTile, kd + (kBlk >> 4), qd + (kBlk >> 4), id, 1);
+      umma_commit(&c.sfull[i]);
+    };
+    auto issue_o_thin = [&](const int i, uint32_t np, uint32_t more) {
+      const uint64_t vd = umma_desc(v_buf(i), kBlk, 1024), pd = umma_desc(p_buf(i), 16, 1024);
+      const uint32_t id = umma_idesc(kThinCols, true, false);
+      // 16 keys at a time: a quarter of P's 64-key blocks of 16 rows
+      for (uint32_t y = 0; y < np; ++y)
+        umma_ss(tmem + 2 * kTile + i * kTile, vd + y * (2048 >> 4),
+                pd + (y >> 2) * (kThinCols * 128 >> 4) + (y & 3) * 2, id, more | y);
     };
     // O += P V, the first or second 64 keys: the first while the softmax is at the others
     auto issue_o = [&](const int i, uint32_t set, uint32_t np, uint32_t more, const int half) {
       const uint32_t s_col = tmem + i * kTile, o_col = tmem + 2 * kTile + i * kTile;
       const uint64_t vd = umma_desc(v_buf(set), kBlk, 1024);
-      const uint32_t id = umma_idesc(kHeadDim, true);
+      const uint32_t id = umma_idesc(kHeadDim, false, true);
       const uint32_t y0 = half * (kTilePages / 2), y1 = half ? np : min(np, (uint32_t)kTilePages / 2);
       if (y1 == y0 + kTilePages / 2) {
         umma_ts4(o_col, s_col + half * 32, vd + half * 4 * (2048 >> 4), id, half ? 1 : more);
@@ -513,6 +551,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     }
     int j = (pairs + 1 - i) / 2;   // fills of this stream's buffers so far
     while (ok && it.next(a, i, g)) {
+      const uint32_t thin = uni(is_thin(a, g));
       ok = mbar_wait(&c.qfull[i], nseg & 1, a.status);
       for (int x = 0; x < g.n && ok; ++x, ++j, ++nt) {
         const int valid = min(kTile, g.keys - (g.t0 + x) * kTile);
@@ -521,7 +560,10 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         ok = mbar_wait(&c.kfull[i], j & 1, a.status);
         if (!ok) break;
         tc_fence_after();
-        issue_s(i, i, np);
+        if (thin)
+          issue_s_thin(i);
+        else
+          issue_s(i, i, np);
         umma_commit(&c.kempty[i]);
         umma_commit(&c.kempty[i]);
         if (last) umma_commit(&c.qempty[i]);
@@ -539,14 +581,19 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
           fence_async_proxy();
           __syncwarp();
         }
-        ok = mbar_wait(&c.phalf[i], nt & 1, a.status);
-        if (!ok) break;
-        tc_fence_after();
-        issue_o(i, i, np, more, 0);
+        if (!thin) {
+          ok = mbar_wait(&c.phalf[i], nt & 1, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_o(i, i, np, more, 0);
+        }
         ok = mbar_wait(&c.pfull[i], nt & 1, a.status);
         if (!ok) break;
         tc_fence_after();
-        issue_o(i, i, np, more, 1);
+        if (thin)
+          issue_o_thin(i, np, more);
+        else
+          issue_o(i, i, np, more, 1);
         umma_commit(&c.vempty[i]);
         umma_commit(&c.vempty[i]);
         if (last) umma_commit(&c.ofull[i]);
@@ -557,7 +604,8 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     umma_commit(&c.drain);
     mbar_wait(&c.drain, 0, a.status);
   } else {
-    // ---- softmax of stream i, one query row per thread
+    // ---- softmax of stream i, one query row per thread (or, thin, one key).  No
+    // step depends on a wait's success: the stream's warps meet at barriers
     const int i = warp >> 2;
     const int r = (warp & 3) * 32 + lane;                       // row of the tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -572,8 +620,120 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         if (seg_rows(a, s, i) > 0) return true;
       return false;
     };
-    bool have = next(g);
-    while (have && ok) {
+    // a thin segment: thread `key` holds that key's scores (then that channel's O) of
+    // all rows, every thread the rows' maxima and its share of their sums
+    const int w4 = warp & 3, key = r, meet = 1 + i;   // hardware barrier of the four warps
+    PdThin& th = c.thin[i];
+    auto thin_seg = [&]() {
+      constexpr int NR = kThin;
+      const int rows = seg_rows(a, g, i);
+      if (w4 == 0 && lane < NR)
+        th.lim[lane] = g.prefix && lane < rows ? min(g.keys, a.L.len(lane / a.G)) : g.keys;
+      bar_sync(meet, 128);   // and P's memory is free of earlier records
+      int low = g.keys;      // keys that every row sees
+      float m[NR], l[NR];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        low = min(low, th.lim[n]);
+        m[n] = -INFINITY;
+        l[n] = 0.f;
+      }
+      for (int x = 0; x < g.n; ++x, ++nt) {
+        ok = ok && mbar_wait(&c.sfull[i], nt & 1, a.status);
+        tc_fence_after();
+        uint32_t s[16];
+        tmem_ld16(s_col, s);
+        tmem_wait_ld();
+        tmem_use16(s);
+        const int at = (g.t0 + x) * kTile + key;
+        if ((g.t0 + x + 1) * kTile > low) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+            if (at >= th.lim[n]) s[n] = __float_as_uint(-INFINITY);
+        }
+        float top[NR];
+        bool up = x == 0;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          top[n] = fmaxf(m[n], redux_max(__uint_as_float(s[n])) * kPdScale);
+          up |= n < rows && top[n] > m[n] + kSlack;
+        }
+        // (on the first tile it is true for all, and the barrier free of others' records)
+        if (bar_any(meet, 128, up)) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+            if (lane == n) th.x[w4][n] = top[n];
+          bar_sync(meet, 128);
+          float f[NR];
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const float t = fmaxf(max3(th.x[0][n], th.x[1][n], th.x[2][n]), th.x[3][n]);
+            f[n] = t == -INFINITY ? 1.f : ex2(m[n] - t);
+            l[n] *= f[n];
+            m[n] = t;
+          }
+          if (x > 0) {   // S is there, so the products before it are complete
+            uint32_t o[16];
+            tmem_ld16(o_col, o);
+            tmem_wait_ld();
+            tmem_use16(o);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n]);
+            tmem_st16(o_col, o);
+            tmem_wait_st();
+          }
+        }
+        // this key's weights: fp16, a column of P (rows of 64 keys, swizzled)
+        const uint32_t dst = p_buf(i) + (key >> 6) * (kThinCols * 128) + (key & 7) * 2;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          const float p = ex2(__fmaf_rn(__uint_as_float(s[n]), kPdScale,
+                                        m[n] == -INFINITY ? 0.f : kLift - m[n]));
+          l[n] += p;
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(
+                           dst + n * 128 + ((((key & 63) >> 3) ^ (n & 7)) * 16)),
+                       "h"(__half_as_ushort(__float2half_rn(p)))
+                       : "memory");
+        }
+        fence_async_proxy();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&c.phalf[i]);
+          mbar_arrive(&c.pfull[i]);
+        }
+      }
+      ok = ok && mbar_wait(&c.ofull[i], nseg & 1, a.status);
+      ++nseg;
+      tc_fence_after();
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float sum = warp_sum(l[n]);
+        if (lane == n) {
+          th.x[w4][n] = sum;
+          if (w4 == 0) th.m[n] = m[n];
+        }
+      }
+      bar_sync(meet, 128);
+      const int64_t at = g.slot * (g.prefix ? a.rows1 : a.G);
+      if (w4 == 0 && lane < rows)
+        (g.prefix ? a.ml1 : a.ml2)[at + lane] =
+            make_float2(th.m[lane] - kLift,
+                        (th.x[0][lane] + th.x[1][lane]) + (th.x[2][lane] + th.x[3][lane]));
+      float* o_dst = (g.prefix ? a.o1 : a.o2) + at * kHeadDim + key;
+      uint32_t o[16];
+      tmem_ld16(o_col, o);
+      tmem_wait_ld();
+      tmem_use16(o);
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+        if (n < rows) o_dst[n * kHeadDim] = __uint_as_float(o[n]);
+    };
+    while (next(g)) {
+      if (is_thin(a, g)) {
+        thin_seg();
+        continue;
+      }
       const int rows = seg_rows(a, g, i);
       const bool busy = (warp & 3) * 32 < rows;   // this warp has rows
       int lim = g.keys;                            // keys this row sees
@@ -628,8 +788,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         l += t.x + t.y;
       };
       for (int x = 0; x < g.n; ++x, ++nt) {
-        ok = mbar_wait(&c.sfull[i], nt & 1, a.status);
-        if (!ok) break;
+        ok = ok && mbar_wait(&c.sfull[i], nt & 1, a.status);
         tc_fence_after();
         bool half = false;   // the first 64 keys' weights are handed over
         if (busy) {
@@ -699,9 +858,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
           mbar_arrive(&c.pfull[i]);
         }
       }
-      if (!ok) break;
-      ok = mbar_wait(&c.ofull[i], nseg & 1, a.status);
-      if (!ok) break;
+      ok = ok && mbar_wait(&c.ofull[i], nseg & 1, a.status);
       ++nseg;
       tc_fence_after();
       if (busy) {
@@ -712,7 +869,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         // eight lanes write 128 bytes of one row
         const int row0 = (warp & 3) * 32, nrow = min(32, rows - row0);
         float* o_dst = (g.prefix ? a.o1 : a.o2) + (at + row0) * kHeadDim;
-        const uint32_t stage = base + 6 * kBuf + kPdCtlBytes + warp * 4096;
+        const uint32_t stage = base + 6 * kBuf + warp * kStage;
 #pragma unroll 1
         for (int y = 0; y < 4; ++y) {
           uint32_t o[32];
@@ -738,7 +895,6 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
           __syncwarp();
         }
       }
-      have = next(g);
     }
   }
   tc_fence_before();

@@ -22,10 +22,11 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint3
          ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: fp16 x fp16 -> fp32, 128 rows, n columns; bmn: B is
-// stored with its n dimension contiguous.
-__device__ __forceinline__ uint32_t umma_idesc(int n, bool bmn) {
-  return (1u << 4) | (bmn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+// Instruction descriptor: fp16 x fp16 -> fp32, 128 rows, n columns; amn, bmn: A
+// is stored with its row dimension contiguous, B with its n dimension.
+__device__ __forceinline__ uint32_t umma_idesc(int n, bool amn, bool bmn) {
+  return (1u << 4) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((128u >> 4) << 24);
 }
 
 // The products below are called by a whole warp, and one elected lane issues
@@ -57,6 +58,16 @@ __device__ __forceinline__ void umma_ts4(uint32_t d, uint32_t a, uint64_t b, uin
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] B[smem], 16 of the summed dimension.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -199,6 +210,28 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+
+// Hardware barrier `id` of n threads; and with the or of their predicates.
+__device__ __forceinline__ void bar_sync(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool bar_any(int id, int n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+// Largest of the warp's values (not NaN).
+__device__ __forceinline__ float redux_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ float ex2(float x) {
