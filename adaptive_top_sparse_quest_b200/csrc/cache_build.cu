@@ -65,16 +65,17 @@ __device__ __forceinline__ void quantize_row(const uint4 raw, const uint32_t (&k
   // rounded quotient, relative; quotients are below 32 (the levels, or 1.5 times
   // as many where the scale is of fp16's smallest values and rounded down), so
   // within 2^-17.  Only a y that is about that near to a half-integer can round to
-  // another code: such a row's lane divides.
+  // another code: such a row's lane divides.  Where a key is infinite or NaN so is
+  // the scale (finite keys' scales are below 2^16), and all codes are 0.
   // 1.5 * 2^23 + y rounds y to the nearest integer, ties to even, into its low
   // bits; the sum of those bits' shifts, less that of the constants, packs them.
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scf));
-  if (scf == 0.0f) inv = 0.0f;   // all codes 0
+  const bool none = !(scf > 0.0f && scf < INFINITY);   // all codes 0
   constexpr float kBig = 12582912.0f;
   uint32_t packed = 0, shifts = 0;
   float d[8];
-  bool near_half = false;
+  bool near_half = none;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j >> 1]));
@@ -88,7 +89,7 @@ __device__ __forceinline__ void quantize_row(const uint4 raw, const uint32_t (&k
     packed = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float y = scf == 0.0f ? 0.0f : fminf(__fdiv_rn(d[j], scf), (float)kLevels);
+      const float y = none ? 0.0f : fminf(__fdiv_rn(d[j], scf), (float)kLevels);
       packed += __float_as_uint(__fadd_rn(y, kBig)) * (1u << (BITS * j));
     }
   }

@@ -239,6 +239,33 @@ def test_write_rows_equals_rebuild(c):
         assert torch.equal(t[still], old[still])
 
 
+@pytest.mark.parametrize("bits", [2, 4])
+def test_quantised_keys_of_infinities_and_nan(bits):
+    """A group of 32 channels that holds an infinity or a NaN has codes of zero
+    (and says so by its scale); every other group is as without it.  Rebuilt and
+    written by slot alike."""
+    from adaptive_top_sparse_quest_b200 import quantize_keys, write_rows
+    kv = _cache(1, 2, 3, False, 40, bits)
+    inf = float("inf")
+    for t, (ch, x) in enumerate([(0, inf), (31, -inf), (40, float("nan")), (64, inf), (65, -inf),
+                                 (127, 65504.0)]):
+        kv.k[0, :, t, ch] = x
+    kv.k[0, 1, 6] = inf
+    kv.seq_lens.fill_(40)
+    keys = quantize_keys(kv)
+    rc, rs, _ = O.quantize_keys(np16(kv.k), bits)
+    bad = ~torch.from_numpy(rs).isfinite()
+    assert bad.sum() == 2 * 5 + 4
+    rc = torch.from_numpy(rc).view(1, 2, 40, 4, -1)
+    rc[bad] = 0
+    assert torch.equal(keys.codes.cpu().view(rc.shape), rc)
+    again = quantize_keys(_cache(1, 2, 3, False, 40, bits))
+    rows = kv.k[0].transpose(0, 1).contiguous()
+    write_rows(kv, rows, rows, torch.arange(40, device="cuda", dtype=torch.int32), again)
+    assert torch.equal(again.codes, keys.codes)
+    assert torch.equal(again.scales.view(torch.int16), keys.scales.view(torch.int16))
+
+
 def test_write_rows_without_keys_or_meta_and_bad_slots():
     from adaptive_top_sparse_quest_b200 import write_rows
     kv = _cache(2, 2, 4, True, 0, 4)
