@@ -57,6 +57,7 @@ constexpr uint32_t kBuf = 2 * kBlk;             // a tile of Q, K or V: 32 KB
 constexpr float kPdScale = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
 constexpr float kLift = 7.f;                    // weights are 2^(s - m + 7), m within 2^8 of the maximum
 constexpr float kSlack = 8.f;
+constexpr float kNone = -1e38f;                 // running maximum before a finite score
 constexpr int kThin = 8;                        // query rows of a thin segment at most
 constexpr int kThinCols = 16;                   // columns of its products (the least there are)
 
@@ -99,7 +100,7 @@ struct PdRange {
 
 struct PdArgs {
   Layout L;
-  const __half* q;
+  const __half *q, *K, *V;
   int Hq, G, P, M;              // M = B * G query rows per KV head
   int pair;                     // the two streams are two row tiles (M > 128)
   int KT, RT;                   // key tiles of the prefix, 256-row tiles per KV head
@@ -255,6 +256,9 @@ __device__ __forceinline__ int seg_rows(const PdArgs& a, const Seg& g, int i) {
 __device__ __forceinline__ bool is_thin(const PdArgs& a, const Seg& g) {
   return !g.prefix || (!a.pair && a.M <= kThin);
 }
+
+// A record's maximum, of the weights without their lift; minus infinity: no record.
+__device__ __forceinline__ float record_max(float m) { return m == kNone ? -INFINITY : m - kLift; }
 
 // A value that is the same in all lanes, in a form that lets the compiler know:
 // it then keeps operand descriptors in uniform registers.
@@ -635,7 +639,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         low = min(low, th.lim[n]);
-        m[n] = -INFINITY;
+        m[n] = kNone;
         l[n] = 0.f;
       }
       for (int x = 0; x < g.n; ++x, ++nt) {
@@ -655,8 +659,8 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         bool up = x == 0;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-          top[n] = fmaxf(m[n], redux_max(__uint_as_float(s[n])) * kPdScale);
-          up |= n < rows && top[n] > m[n] + kSlack;
+          top[n] = max2(m[n], redux_max(__uint_as_float(s[n])) * kPdScale);
+          up |= n < rows && !(top[n] <= m[n] + kSlack);
         }
         // (on the first tile it is true for all, and the barrier free of others' records)
         if (bar_any(meet, 128, up)) {
@@ -667,8 +671,8 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
           float f[NR];
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
-            const float t = fmaxf(max3(th.x[0][n], th.x[1][n], th.x[2][n]), th.x[3][n]);
-            f[n] = t == -INFINITY ? 1.f : ex2(m[n] - t);
+            const float t = max2(max3(th.x[0][n], th.x[1][n], th.x[2][n]), th.x[3][n]);
+            f[n] = ex2(m[n] - t);
             l[n] *= f[n];
             m[n] = t;
           }
@@ -687,8 +691,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         const uint32_t dst = p_buf(i) + (key >> 6) * (kThinCols * 128) + (key & 7) * 2;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-          const float p = ex2(__fmaf_rn(__uint_as_float(s[n]), kPdScale,
-                                        m[n] == -INFINITY ? 0.f : kLift - m[n]));
+          const float p = ex2(__fmaf_rn(__uint_as_float(s[n]), kPdScale, kLift - m[n]));
           l[n] += p;
           asm volatile("st.shared.u16 [%0], %1;" ::"r"(
                            dst + n * 128 + ((((key & 63) >> 3) ^ (n & 7)) * 16)),
@@ -718,7 +721,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       const int64_t at = g.slot * (g.prefix ? a.rows1 : a.G);
       if (w4 == 0 && lane < rows)
         (g.prefix ? a.ml1 : a.ml2)[at + lane] =
-            make_float2(th.m[lane] - kLift,
+            make_float2(record_max(th.m[lane]),
                         (th.x[0][lane] + th.x[1][lane]) + (th.x[2][lane] + th.x[3][lane]));
       float* o_dst = (g.prefix ? a.o1 : a.o2) + at * kHeadDim + key;
       uint32_t o[16];
@@ -738,16 +741,16 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       const bool busy = (warp & 3) * 32 < rows;   // this warp has rows
       int lim = g.keys;                            // keys this row sees
       if (g.prefix && r < rows) lim = min(lim, a.L.len((first_row(a, g, i) + r) / a.G));
-      float m = -INFINITY, l = 0.f;
+      float m = kNone, l = 0.f;
       // raise the running maximum (log2 units) to the tile's; past kSlack, or
       // on the first tile, it is taken over and what is summed so far rescaled
       auto raise = [&](const float* mx, bool first) {
-        const float top = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * kPdScale);
+        const float top = max2(m, max3(max2(mx[0], mx[1]), mx[2], mx[3]) * kPdScale);
         if (first) {
           m = top;
-        } else if (__any_sync(0xffffffffu, r < rows && top > m + kSlack)) {
+        } else if (__any_sync(0xffffffffu, r < rows && !(top <= m + kSlack))) {
           // S is there, so the products before it are complete: O may be rescaled
-          const float f = top == -INFINITY ? 1.f : ex2(m - top);
+          const float f = ex2(m - top);
           l *= f;
           m = top;
 #pragma unroll 1
@@ -842,7 +845,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
               max32(s, mx);
             }
             raise(mx, x == 0);
-            const float lift = m == -INFINITY ? 0.f : kLift - m;
+            const float lift = kLift - m;
 #pragma unroll 1
             for (int y = 0; y < nch; ++y) {
               load(y);
@@ -864,7 +867,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       if (busy) {
         const int per = g.prefix ? a.rows1 : a.G;
         const int64_t at = g.slot * per + (g.prefix && a.pair ? i * kTile : 0);
-        if (r < rows) (g.prefix ? a.ml1 : a.ml2)[at + r] = make_float2(m - kLift, l);
+        if (r < rows) (g.prefix ? a.ml1 : a.ml2)[at + r] = make_float2(record_max(m), l);
         // 32 columns of the warp's rows at a time, through shared memory, so that
         // eight lanes write 128 bytes of one row
         const int row0 = (warp & 3) * 32, nrow = min(32, rows - row0);
@@ -911,6 +914,48 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinMany = 12;
+
+// Output row bh (KV head h) by one warp alone, from sequence 0's first len rows:
+// a key per lane, then four channels per lane.
+__device__ __forceinline__ void row_alone(const PdArgs& a, int h, int64_t bh, int len, float& M,
+                                       float& Ls, float4& A) {
+  const int lane = threadIdx.x & 31;
+  const __half2* q = reinterpret_cast<const __half2*>(a.q + bh * kHeadDim);
+  M = -INFINITY;
+  Ls = 0.f;
+  A = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int t0 = 0; t0 < len; t0 += 32) {
+    const int t = min(t0 + lane, len - 1), n = min(32, len - t0);
+    const int64_t row = a.L.page_row(0, h, t / kPage) + t % kPage;
+    const __half2* k = reinterpret_cast<const __half2*>(a.K + row * kHeadDim);
+    float s = 0.f;
+#pragma unroll 8
+    for (int z = 0; z < kHeadDim / 2; ++z) {
+      const float2 x = __half22float2(q[z]), y = __half22float2(k[z]);
+      s = __fmaf_rn(x.y, y.y, __fmaf_rn(x.x, y.x, s));
+    }
+    s = lane < n ? s * kPdScale : -INFINITY;
+    const float top = fmaxf(M, warp_max(s));
+    const float keep = M == -INFINITY ? 0.f : ex2(M - top);
+    const float p = s == -INFINITY ? 0.f : ex2(s - top);
+    M = top;
+    Ls = Ls * keep + warp_sum(p);
+    A.x *= keep;
+    A.y *= keep;
+    A.z *= keep;
+    A.w *= keep;
+    for (int j = 0; j < n; ++j) {
+      const float f = __shfl_sync(0xffffffffu, p, j);
+      const __half2* v = reinterpret_cast<const __half2*>(
+          a.V + __shfl_sync(0xffffffffu, row, j) * kHeadDim + 4 * lane);
+      const float2 v0 = __half22float2(v[0]), v1 = __half22float2(v[1]);
+      A.x = __fmaf_rn(f, v0.x, A.x);
+      A.y = __fmaf_rn(f, v0.y, A.y);
+      A.z = __fmaf_rn(f, v1.x, A.z);
+      A.w = __fmaf_rn(f, v1.y, A.w);
+    }
+  }
+}
 
 template <int W>
 __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_constant__ PdArgs a) {
@@ -990,7 +1035,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
         v = __ldcg((own ? a.ml2 : a.ml1) + at);
     }
     const float top = fmaxf(M, warp_max(v.x));
-    if (top == -INFINITY) continue;
+    if (!__any_sync(0xffffffffu, v.x != -INFINITY)) continue;
     const float keep = M == -INFINITY ? 0.f : ex2(M - top);
     const float f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
     M = top;
@@ -1043,12 +1088,17 @@ __global__ void __launch_bounds__(kJoinThreads) k_prefix_join(const __grid_const
       A.w = __fmaf_rn(e.w, f, A.w);
     }
   }
-  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+  // A row that ends inside the prefix has weights of zero for the rows of V past
+  // its end, which its tiles hold for other sequences: an infinity or a NaN there
+  // would still reach it.  Its result then tells, and it is done again by itself.
+  if (len < a.P && !__all_sync(0xffffffffu, fabsf((A.x + A.y) + (A.z + A.w)) < INFINITY))
+    row_alone(a, h, bh, len, M, Ls, A);
+  const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
   const __half2 r[2] = {__floats2half2_rn(A.x * inv, A.y * inv),
                         __floats2half2_rn(A.z * inv, A.w * inv)};
   *reinterpret_cast<uint2*>(a.out + (int64_t)bh * kHeadDim + 4 * lane) = *reinterpret_cast<const uint2*>(r);
   if (a.lse && lane == 0)
-    a.lse[bh] = Ls > 0.f ? (M + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+    a.lse[bh] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * 0.6931471805599453f;
 }
 
 // Workspace: status word | CTA ranges | own tiles before each sequence |
@@ -1141,6 +1191,8 @@ cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int p
   std::memset(&a, 0, sizeof(a));
   a.L = L;
   a.q = q;
+  a.K = K;
+  a.V = V;
   a.Hq = Hq;
   a.G = Hq / L.Hk;
   a.P = prefix_len;

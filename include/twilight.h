@@ -438,8 +438,10 @@ int tw_write_rows(const tw_kv* kv, const uint16_t* k_new, int64_t k_stride,
  * others from each sequence's own.  prefix_len is a multiple of 16 in
  * [0, max_seq_len]; 0 shares nothing (plain dense decode).  A sequence shorter
  * than the prefix attends to its first len_b tokens; an empty one gives out = 0
- * and lse = -inf.  Rows at and past a sequence's end are not used, whatever
- * they hold (NaN included).  Cache rows must number below 2^31.  Workspace:
+ * and lse = -inf.  Rows at and past a sequence's end do not reach its result,
+ * whatever they hold (NaN included; infinite or NaN values in the prefix past the
+ * end of a shorter sequence cost that one a slow pass of its own).  A score of
+ * NaN or +inf makes a row NaN; scores of -inf count nothing.  Cache rows must number below 2^31.  Workspace:
  * tw_prefix_workspace_size bytes.
  */
 int tw_prefix_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,

@@ -482,6 +482,71 @@ def test_prefix_decode_back_to_back_with_changing_inputs():
         check_attention(qs[i], k, v, table, all_lens[i].tolist(), outs[i], lses[i])
 
 
+@pytest.mark.parametrize("B", [2, 3, 40])
+@pytest.mark.parametrize("paged", [False, True])
+def test_prefix_decode_non_finite_rows(B, paged):
+    """A NaN in a key that a row sees makes that row NaN; a key whose score is
+    minus infinity does not count, plus infinity is NaN; rows of V past the end
+    of a sequence inside the prefix do not reach it, whatever they hold.  On
+    two of four KV heads; the others are as without it."""
+    Hq, Hk, P, G = 16, 4, 400, 4
+    lens = [(500, 90, 300, 420, 0, 399)[i % 6] + i // 6 for i in range(B)]
+    c = dict(Hq=Hq, Hk=Hk, P=P, lens=lens, paged=paged)
+    step, (q, k, v, table, dl) = _run_prefix(c)
+    q[..., 7] = torch.where(q[..., 7] < 0, -1.0, 1.0)
+    def row(x, b, t):     # [Hk][128] of token t
+        return x[table[b, t // PAGE].long(), :, t % PAGE] if paged else x[b, :, t]
+    nan, inf = float("nan"), float("inf")
+    row(v, 0, 310)[0, 5:9] = inf       # head 0: values in the prefix that shorter ones do not see
+    row(v, 0, 399)[0, 100] = nan
+    row(k, 0, 350)[1, 3] = nan         # head 1: a key of the prefix, and one of sequence 0's own
+    row(k, 0, 450)[1, 9] = nan
+    for t in range(128, 256):          # head 2: a whole tile of infinite scores
+        row(k, 0, t)[2, 7] = inf
+    if not paged:                      # the prefix is the same rows for all
+        k[:, :, :P], v[:, :, :P] = k[:1, :, :P].clone(), v[:1, :, :P].clone()
+    step(q)
+    _check_status(step)
+    out, lse = step.out.view(B, Hk, G, D), step.lse.view(B, Hk, G)
+    sees = torch.tensor(lens, device="cuda")
+    bad = torch.zeros(B, Hk, G, dtype=torch.bool, device="cuda")
+    bad[:, 1] = (sees > 350)[:, None]
+    up = q.view(B, Hk, G, D)[:, 2, :, 7] > 0
+    bad[:, 2] = up & (sees > 128)[:, None]
+    assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
+    for b in range(B):
+        n = lens[b]
+        z0 = out[b, 0]
+        if n > 310:
+            assert not bool(z0[:, 5:9].isfinite().any())
+        if n > 399:
+            assert bool(z0[:, 100].isnan().all())
+        seen = [x for t, x in ((310, [5, 6, 7, 8]), (399, [100])) if n > t for x in x]
+        rest = [x for x in range(D) if x not in seen]
+        assert bool(z0[:, rest].isfinite().all()), (b, n)
+    # the other rows against the reference, head 2's without the tile that does not count
+    for b in range(B):
+        n = lens[b]
+        for h in range(Hk):
+            kb, vb = k[:, h:h + 1], v[:, h:h + 1]
+            tb = table[b:b + 1] if paged else None
+            if not paged:
+                kb, vb = kb[b:b + 1], vb[b:b + 1]
+            if h == 0 and n > 310:
+                continue
+            if h == 2 and n >= 256:
+                n -= 128
+                if paged:
+                    tb = torch.cat([tb[:, :8], tb[:, 16:]], 1)
+                else:
+                    kb, vb = (torch.cat([x[:, :, :128], x[:, :, 256:]], 2) for x in (kb, vb))
+            good = ~bad[b, h]
+            if bool(good.any()):
+                check_attention(q.view(B, Hk, G, D)[b:b + 1, h][:, good], kb, vb, tb, [n],
+                                out[b:b + 1, h][:, good], lse[b:b + 1, h][:, good])
+            n = lens[b]
+
+
 def test_prefix_decode_hostile_table_and_lengths():
     """Lengths outside [0, N] are clamped; page ids outside the pool read some
     page of it, which spoils that sequence and no other."""
