@@ -60,36 +60,36 @@ __device__ __forceinline__ void quantize_row(const uint4 raw, const uint32_t (&k
   const float s32 = __fdiv_rn(__fsub_rn(mxf, mnf), (float)kLevels);
   const __half sc = __float2half_rn(s32);
   const float scf = __half2float(sc);
-  // code = min(rint(fl((x - mn) / scale)), levels).  The product y with the
-  // approximate reciprocal (off by 2^-23 of itself at most) is within 2^-22 of the
-  // rounded quotient, relative; quotients are below 32 (the levels, or 1.5 times
-  // as many where the scale is of fp16's smallest values and rounded down), so
-  // within 2^-17.  Only a y that is about that near to a half-integer can round to
-  // another code: such a row's lane divides.  Where a key is infinite or NaN so is
-  // the scale (finite keys' scales are below 2^16), and all codes are 0.
-  // 1.5 * 2^23 + y rounds y to the nearest integer, ties to even, into its low
-  // bits; the sum of those bits' shifts, less that of the constants, packs them.
+  // code = min(rint(fl((x - mn) / scale)), levels).  With the approximate
+  // reciprocal (off by 2^-23 of itself at most) made 2^-21 smaller and larger, the
+  // two products enclose the rounded quotient: where they round to one integer,
+  // the quotient does too; a lane with a value that lies between divides.
+  // 1.5 * 2^23 + y, fused, rounds y to the nearest integer, ties to even, into its
+  // low bits; the sum of those bits' shifts, less that of the constants, packs
+  // them.  Where a key is infinite or NaN so is the scale (finite keys' scales are
+  // below 2^16), and all codes are 0, as they are for a scale of 0.
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scf));
-  const bool none = !(scf > 0.0f && scf < INFINITY);   // all codes 0
+  if (scf == 0.0f) inv = 0.0f;
+  const bool finite = scf < INFINITY;
   constexpr float kBig = 12582912.0f;
-  uint32_t packed = 0, shifts = 0;
+  const float inv_lo = inv * (1.0f - 0x1p-21f), inv_hi = inv * (1.0f + 0x1p-21f);
+  uint32_t packed = 0, shifts = 0, apart = finite ? 0u : 1u;
   float d[8];
-  bool near_half = none;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j >> 1]));
     d[j] = __fsub_rn(j & 1 ? x.y : x.x, mnf);
-    const float y = fminf(__fmul_rn(d[j], inv), (float)kLevels), z = __fadd_rn(y, kBig);
-    near_half |= fabsf(__fsub_rn(y, __fsub_rn(z, kBig))) > 0.5f - 0x1p-15f;
-    packed += __float_as_uint(z) * (1u << (BITS * j));
+    const uint32_t z = __float_as_uint(__fmaf_rn(d[j], inv_lo, kBig));
+    apart |= z ^ __float_as_uint(__fmaf_rn(d[j], inv_hi, kBig));
+    packed += min(z, 0x4B400000u + kLevels) * (1u << (BITS * j));
     shifts += 0x4B400000u * (1u << (BITS * j));
   }
-  if (near_half) {
+  if (apart) {
     packed = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float y = none ? 0.0f : fminf(__fdiv_rn(d[j], scf), (float)kLevels);
+      const float y = scf > 0.0f && finite ? fminf(__fdiv_rn(d[j], scf), (float)kLevels) : 0.0f;
       packed += __float_as_uint(__fadd_rn(y, kBig)) * (1u << (BITS * j));
     }
   }
@@ -205,71 +205,59 @@ k_append_keys(Layout L, const __half* __restrict__ K, uint8_t* __restrict__ code
 // page's min / max is folded, so K is read once instead of three times.
 //
 // A run of list neighbours on consecutive slots of one page is one warp's work
-// per KV head, a row per half-warp at a time: it alone touches that page's metadata, so no atomics are
-// needed and the result does not depend on an order.  The run that starts at a
-// page's first row starts its metadata anew; another folds what is there (its
-// earlier rows are in it).  A block looks at `chunk` list places and takes the
-// runs that start there, to their ends up to 15 places further on.
-constexpr int kWrThreads = 256;
-constexpr int kWrHeads = 16;  // KV heads per block
+// per KV head, a row per half-warp at a time: it alone touches that page's
+// metadata, so no atomics are needed and the result does not depend on an order.
+// The run that starts at a page's first row starts its metadata anew; another
+// folds what is there (its earlier rows are in it).  A warp looks at `chunk` list
+// places, for one head, and takes the runs that start there, to their ends up to
+// 15 places further on; it needs no other warp, so a block is only what shares a
+// launch slot.
+//
+// What bounds it (4 bits, one B200): the instructions of the quantiser, 0.6 of the
+// issue slots while rows are there, and latency around them.  8191 tokens x 8
+// heads: 21 us (11 by the bytes at the copy rate); 20000 x 32 at 2 bits: 128 (108);
+// 64 single tokens x 8 heads: 3.0, one chain of loads.
+constexpr int kWrThreads = 128;
+constexpr int kWrWarps = kWrThreads / 32;
 constexpr int kWrRows = 2;   // rows of a run in flight per half-warp
 
 template <int BITS>
-__global__ void __launch_bounds__(kWrThreads, 4)
+__global__ void __launch_bounds__(kWrThreads, 8)
 k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restrict__ v_new,
              int64_t k_stride, int64_t v_stride, const int32_t* __restrict__ slots, int T,
              int chunk, __half* __restrict__ K, __half* __restrict__ V,
              uint8_t* __restrict__ codes, __half* __restrict__ scales, __half* __restrict__ zeros,
              __half* __restrict__ meta) {
-  __shared__ int sl[kWrMaxChunk + kPage + 1];   // slots of places t0 - 1 .. t0 + chunk + 14
-  __shared__ int run_at[kWrMaxChunk], run_n[kWrMaxChunk];
-  __shared__ int nruns;
-  const int tid = threadIdx.x, lane = tid & 31, l16 = tid & 15;
+  const int tid = threadIdx.x, lane = tid & 31, l16 = tid & 15, hw = lane >> 4;
   const unsigned hmask = 0xFFFFu << (lane & 16);
-  const int64_t t0 = (int64_t)blockIdx.x * chunk;
+  const uint32_t item = blockIdx.x * kWrWarps + (tid >> 5), ck = item / (uint32_t)L.Hk;
+  const int h = (int)(item - ck * L.Hk);
+  // lane l holds place t0 - 1 + l
+  const int64_t t0 = (int64_t)ck * chunk, t = t0 - 1 + lane;
   const int nslot = L.page_table ? L.pool_pages * kPage : L.B * L.N;
-  if (tid < chunk + kPage) {
-    const int64_t t = t0 - 1 + tid;
-    const int s = t >= 0 && t < T ? slots[t] : -1;
-    sl[tid] = (unsigned)s < (unsigned)nslot ? s : -1;
-  }
-  if (tid == 0) nruns = 0;
-  __syncthreads();
-  // position of a slot within its sequence (paged: its pool page)
-  auto offset = [&](int s) { return L.page_table ? s % kPage : s % L.N; };
-  if (tid < chunk && sl[tid + 1] >= 0) {
-    const int s = sl[tid + 1], o = offset(s) % kPage;
-    const bool starts = o == 0 || sl[tid] != s - 1;
-    if (starts) {
-      // rows left in the page; a contiguous sequence may end before its page does
-      const int left = L.page_table ? kPage - o : min(kPage - o, L.N - offset(s));
-      int n = 1;
-      while (n < left && sl[tid + 1 + n] == s + n) ++n;
-      const int r = atomicAdd(&nruns, 1);   // the runs' order does not matter
-      run_at[r] = tid;
-      run_n[r] = n;
-    }
-  }
-  __syncthreads();
-  const int h0 = blockIdx.y * kWrHeads;
-  const int nh = min(kWrHeads, L.Hk - h0);
-  const int hw = lane >> 4;
-  for (int i = tid >> 5; i < nruns * nh; i += kWrThreads / 32) {
-    const int r = i / nh, h = h0 + i % nh;
-    const int n = run_n[r], s = sl[run_at[r] + 1];
-    const int64_t tok = t0 + run_at[r];
+  int s = lane <= chunk + kPage - 1 && t >= 0 && t < T ? slots[t] : -1;
+  if ((unsigned)s >= (unsigned)nslot) s = -1;
+  const int prev = __shfl_up_sync(0xffffffffu, s, 1);
+  // a place carries its neighbour's run on unless a page (or sequence) begins there
+  const bool first = s < 0 || (L.page_table ? s : s % L.N) % kPage == 0;
+  const unsigned on = __ballot_sync(0xffffffffu, lane > 0 && !first && prev == s - 1);
+  unsigned starts = __ballot_sync(0xffffffffu, s >= 0 && lane > 0 && lane <= chunk) & ~on;
+  for (; starts; starts &= starts - 1) {
+    const int at = __ffs(starts) - 1, n = __ffs(~(on >> (at + 1)));
+    const int slot = __shfl_sync(0xffffffffu, s, at);
+    const int64_t tok = t0 - 1 + at;
     int64_t row, mrec;
     int o;
     if (L.page_table) {
-      o = s % kPage;
-      mrec = (int64_t)(s / kPage) * L.Hk + h;
+      o = slot % kPage;
+      mrec = (int64_t)(slot / kPage) * L.Hk + h;
       row = mrec * kPage + o;
     } else {
-      const int t = s % L.N;
-      o = t % kPage;
-      const int64_t bh = (int64_t)(s / L.N) * L.Hk + h;
-      row = bh * L.N + t;
-      mrec = bh * L.max_pages + t / kPage;
+      const int pos = slot % L.N;
+      o = pos % kPage;
+      const int64_t bh = (int64_t)(slot / L.N) * L.Hk + h;
+      row = bh * L.N + pos;
+      mrec = bh * L.max_pages + pos / kPage;
     }
     const __half* ks = k_new + tok * k_stride + h * kHeadDim + l16 * 8;
     const __half* vs = v_new + tok * v_stride + h * kHeadDim + l16 * 8;
@@ -279,6 +267,9 @@ k_write_rows(Layout L, const __half* __restrict__ k_new, const __half* __restric
       kmin[j] = 0x7FFF7FFFu;
       kmax[j] = 0x80008000u;
     }
+    // (the rows in flight are quantised together, which hides the arithmetic's
+    // latency; loads sent ahead of the row before them instead: 21 -> 24 us for a
+    // prompt of 8191 tokens and 8 heads)
     for (int c = hw; c < n; c += 2 * kWrRows) {
       uint4 kr[kWrRows], vr[kWrRows];
 #pragma unroll
@@ -411,12 +402,14 @@ cudaError_t launch_write_rows(const Layout& L, const __half* k_new, const __half
                               int64_t k_stride, int64_t v_stride, const int32_t* slots, int T,
                               __half* K, __half* V, uint8_t* codes, __half* scales, __half* zeros,
                               __half* meta, cudaStream_t st, int num_sms) {
-  // list places per block: as many as a page has rows, fewer while the grid
-  // would not give every SM four blocks (single tokens are a run each; of a
-  // prompt's places only every 16th starts a run)
-  int chunk = kWrMaxChunk;
-  while (chunk > 1 && (T + chunk - 1) / chunk < 4 * num_sms) chunk /= 2;
-  const dim3 grid((T + chunk - 1) / chunk, (L.Hk + kWrHeads - 1) / kWrHeads);
+  // list places per warp: as many as a page has rows, fewer while there would
+  // not be 16 warps for every SM: single tokens are a run each (1024 x 8 heads: 7.2
+  // us, 14.9 with 4 warps per SM asked for), of a prompt's places only every 16th
+  // starts one (2000 x 8 heads: 10.0, 11.9 with 64)
+  int chunk = kPage;
+  auto items = [&] { return (int64_t)((T + chunk - 1) / chunk) * L.Hk; };
+  while (chunk > 1 && items() < 16 * num_sms) chunk /= 2;
+  const dim3 grid((unsigned)((items() + kWrWarps - 1) / kWrWarps));
   return launch_k(L.kbits == 2 ? k_write_rows<2> : k_write_rows<4>, grid, dim3(kWrThreads), 0, st,
                   false, L, k_new, v_new, k_stride, v_stride, slots, T, chunk, K, V, codes, scales,
                   zeros, meta);

@@ -732,7 +732,7 @@ int tw_write_rows(const tw_kv* kv, const uint16_t* k_new, int64_t k_stride,
     return TW_ERR_INVALID_ARG;
   const int64_t nslots =
       L.page_table ? (int64_t)L.pool_pages * tw::kPage : (int64_t)L.B * L.N;
-  if (nslots > INT32_MAX) return TW_ERR_UNSUPPORTED;
+  if (nslots > INT32_MAX || (int64_t)num_tokens * L.Hk > INT32_MAX) return TW_ERR_UNSUPPORTED;
   if (num_tokens == 0 || nslots == 0) return TW_OK;
   int sms = 0;
   TW_TRY(device_check(&sms));

@@ -129,7 +129,6 @@ cudaError_t launch_resolve_rows(const Layout& L, int Hq, int group_sets, const i
 
 
 // Rows written by slot (cache_build.cu).
-constexpr int kWrMaxChunk = 16;
 cudaError_t launch_write_rows(const Layout& L, const __half* k_new, const __half* v_new,
                               int64_t k_stride, int64_t v_stride, const int32_t* slots, int T,
                               __half* K, __half* V, uint8_t* codes, __half* scales, __half* zeros,

@@ -421,7 +421,8 @@ int tw_update_page_table(int32_t batch, const int32_t* seq_lens, const int32_t* 
  * listed in two places leaves that page's rows or metadata unspecified.
  * kv->k and kv->v are written; kv->seq_lens and the entries of
  * kv->page_table are not read (page_table only tells the layout).  k_new and
- * v_new may not overlap the cache.  The cache's slots must number below 2^31.
+ * v_new may not overlap the cache.  The cache's slots and num_tokens * Hk must
+ * be below 2^31.
  */
 int tw_write_rows(const tw_kv* kv, const uint16_t* k_new, int64_t k_stride,
                   const uint16_t* v_new, int64_t v_stride, const int32_t* slots,
