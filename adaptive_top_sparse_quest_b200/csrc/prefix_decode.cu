@@ -25,21 +25,25 @@
 //     when a row's maximum has risen by more than 2^8: the weights are lifted to
 //     between 2^7 and 2^15 at the maximum, so that they fit fp16, and what falls
 //     below its normal range is below 2^-21 of the row's largest.
+// Segments of at most eight query rows (a sequence's own tokens, small batches)
+// are turned round, keys along the tensor cores' rows: see is_thin().
 // With more than 128 query rows per KV head the two streams are two row tiles on
 // the same K / V buffers, which halves the traffic, and one stream's softmax runs
 // while the other's products do; with fewer they take separate tiles of keys.
 // Tensor memory: S0 | S1 | O0 | O1, 128 columns each.
 //
-// What bounds it (one B200; both kernels, sustained, in us):
+// What bounds it (one B200; whole calls, in us, in a loop of them):
 //   - few query rows (16 sequences of 1000 .. 9000 tokens, nothing shared): HBM;
-//     the tile kernel reads 307 MB in 54, 0.87 of the measured copy rate, and the
-//     call takes 63 with its start, the join and the gap between the two;
+//     307 MB take 59, of which the copies 54 (0.87 of the measured copy rate) and
+//     the start, the join and the gap between the two kernels the rest;
 //   - 512 rows per head (128 sequences behind 128k tokens): power.  A tile of 256
 //     rows takes 2930 clocks, 2048 of them tensor-core time, and the clock falls
-//     to 1.3 GHz at the 1000 W cap: 340, 0.81 PFLOP/s; started cold 250;
-//   - 256 rows (64 behind 32k): both, and the 19 MB of records written and read;
-//   - small calls: latency: set-up 2, first copies 2, a tile's chain 2, the
-//     records and the join 6.
+//     to 1.3 GHz at the 1000 W cap: 330, 0.83 PFLOP/s; started cold 250;
+//   - 256 rows (64 behind 32k): both (74), and the 19 MB of records written and
+//     read; the tensor cores are busy for a third of the tile kernel's clocks;
+//   - many short own parts (16 sequences of a multi-head layer): 46, 31 by bytes;
+//   - small calls (15 .. 18): latency: set-up 2, first copies 2, a tile's chain 2,
+//     the records and the join 6.
 #include <cstring>
 
 #include "tw_common.cuh"
@@ -252,7 +256,9 @@ __device__ __forceinline__ int seg_rows(const PdArgs& a, const Seg& g, int i) {
 // O^T += V^T P^T, keys and then channels along the tensor cores' 128 rows and the
 // query rows along 16 columns.  A product then costs a quarter or less (it is
 // bound by reading K or V from shared memory, 256 clocks a tile) and the softmax
-// has a key per thread instead of a row of 128 keys.
+// has a key per thread instead of a row of 128 keys.  Eight covers every own part
+// (G <= 8) in registers a thread has left.  (16 sequences, nothing shared: 58.2 us,
+// 61.5 with one form for all; 64 behind 32k tokens: 71.5, 76.)
 __device__ __forceinline__ bool is_thin(const PdArgs& a, const Seg& g) {
   return !g.prefix || (!a.pair && a.M <= kThin);
 }
