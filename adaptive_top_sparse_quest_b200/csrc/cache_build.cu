@@ -66,31 +66,42 @@ __device__ __forceinline__ void quantize_row(const uint4 raw, const uint32_t (&k
   // the quotient does too; a lane with a value that lies between divides.
   // 1.5 * 2^23 + y, fused, rounds y to the nearest integer, ties to even, into its
   // low bits; the sum of those bits' shifts, less that of the constants, packs
-  // them.  Where a key is infinite or NaN so is the scale (finite keys' scales are
-  // below 2^16), and all codes are 0, as they are for a scale of 0.
+  // them.  A lane divides as well where the scale is no normal fp16 number: where
+  // a key is infinite or NaN the scale is (finite keys' are below 2^16), and all
+  // codes are 0; a subnormal one may be rounded down so far that quotients pass the
+  // levels (a normal one is within 2^-11, and 15 (1 + 2^-11) rounds to 15).  Scale
+  // 0, all keys alike, gives codes of 0 by a reciprocal of 0.
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scf));
   if (scf == 0.0f) inv = 0.0f;
-  const bool finite = scf < INFINITY;
+  const bool plain = scf == 0.0f || (scf >= 0x1p-14f && scf < INFINITY);
   constexpr float kBig = 12582912.0f;
-  const float inv_lo = inv * (1.0f - 0x1p-21f), inv_hi = inv * (1.0f + 0x1p-21f);
-  uint32_t packed = 0, shifts = 0, apart = finite ? 0u : 1u;
-  float d[8];
+  const float lo1 = inv * (1.0f - 0x1p-21f), hi1 = inv * (1.0f + 0x1p-21f);
+  const uint64_t inv_lo = f2_pack(lo1, lo1), inv_hi = f2_pack(hi1, hi1);
+  const uint64_t big = f2_pack(kBig, kBig), sub = f2_pack(-mnf, -mnf);
+  uint32_t packed = 0, shifts = 0, apart = plain ? 0u : 1u;
+  uint64_t d[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j >> 1]));
-    d[j] = __fsub_rn(j & 1 ? x.y : x.x, mnf);
-    const uint32_t z = __float_as_uint(__fmaf_rn(d[j], inv_lo, kBig));
-    apart |= z ^ __float_as_uint(__fmaf_rn(d[j], inv_hi, kBig));
-    packed += min(z, 0x4B400000u + kLevels) * (1u << (BITS * j));
-    shifts += 0x4B400000u * (1u << (BITS * j));
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+    d[j] = f2_add(f2_pack(x.x, x.y), sub);
+    const float2 z = f2_unpack(f2_fma(d[j], inv_lo, big)), y = f2_unpack(f2_fma(d[j], inv_hi, big));
+    apart |= __float_as_uint(z.x) ^ __float_as_uint(y.x);
+    apart |= __float_as_uint(z.y) ^ __float_as_uint(y.y);
+    packed += __float_as_uint(z.x) * (1u << (2 * BITS * j));
+    packed += __float_as_uint(z.y) * (1u << (2 * BITS * j + BITS));
+    shifts += 0x4B400000u * ((1u << (2 * BITS * j)) + (1u << (2 * BITS * j + BITS)));
   }
   if (apart) {
     packed = 0;
+    const bool some = scf > 0.0f && scf < INFINITY;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float y = scf > 0.0f && finite ? fminf(__fdiv_rn(d[j], scf), (float)kLevels) : 0.0f;
-      packed += __float_as_uint(__fadd_rn(y, kBig)) * (1u << (BITS * j));
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = f2_unpack(d[j]);
+      const float y0 = some ? fminf(__fdiv_rn(x.x, scf), (float)kLevels) : 0.0f;
+      const float y1 = some ? fminf(__fdiv_rn(x.y, scf), (float)kLevels) : 0.0f;
+      packed += __float_as_uint(__fadd_rn(y0, kBig)) * (1u << (2 * BITS * j));
+      packed += __float_as_uint(__fadd_rn(y1, kBig)) * (1u << (2 * BITS * j + BITS));
     }
   }
   packed -= shifts;
@@ -98,20 +109,9 @@ __device__ __forceinline__ void quantize_row(const uint4 raw, const uint32_t (&k
     *reinterpret_cast<uint32_t*>(codes + row * (kHeadDim / 2) + l16 * 4) = packed;
   else
     *reinterpret_cast<uint16_t*>(codes + row * (kHeadDim / 4) + l16 * 2) = (uint16_t)packed;
-  // gather the 4 groups' scale / zero to lane 0 of the half-warp: one 8-byte store each
-  const uint32_t sc_bits = __half_as_ushort(sc);
-  const int base = lane & 16;
-  uint32_t s[4], z[4];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    s[g] = __shfl_sync(hmask, sc_bits, base + 4 * g);
-    z[g] = __shfl_sync(hmask, mn_bits, base + 4 * g);
-  }
-  if (l16 == 0) {
-    *reinterpret_cast<uint2*>(scales + row * kGroups) =
-        make_uint2(s[0] | (s[1] << 16), s[2] | (s[3] << 16));
-    *reinterpret_cast<uint2*>(zeros + row * kGroups) =
-        make_uint2(z[0] | (z[1] << 16), z[2] | (z[3] << 16));
+  if ((l16 & 3) == 0) {   // a group's first lane
+    scales[row * kGroups + (l16 >> 2)] = sc;
+    zeros[row * kGroups + (l16 >> 2)] = __ushort_as_half((unsigned short)mn_bits);
   }
 }
 
@@ -215,8 +215,8 @@ k_append_keys(Layout L, const __half* __restrict__ K, uint8_t* __restrict__ code
 //
 // What bounds it (4 bits, one B200): the instructions of the quantiser, 0.6 of the
 // issue slots while rows are there, and latency around them.  8191 tokens x 8
-// heads: 21 us (11 by the bytes at the copy rate); 20000 x 32 at 2 bits: 128 (108);
-// 64 single tokens x 8 heads: 3.0, one chain of loads.
+// heads: 19.3 us (11 by the bytes at the copy rate); 20000 x 32 at 2 bits: 121 (108);
+// 64 single tokens x 8 heads: 2.8, one chain of loads.
 constexpr int kWrThreads = 128;
 constexpr int kWrWarps = kWrThreads / 32;
 constexpr int kWrRows = 2;   // rows of a run in flight per half-warp

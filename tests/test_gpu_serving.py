@@ -266,6 +266,33 @@ def test_quantised_keys_of_infinities_and_nan(bits):
     assert torch.equal(again.scales.view(torch.int16), keys.scales.view(torch.int16))
 
 
+@pytest.mark.parametrize("bits", [2, 4])
+def test_quantised_keys_of_all_ranges_and_ties(bits):
+    """Codes, scales and zeros equal the definition's for groups whose ranges run
+    from fp16's smallest values to its largest, and for keys half-way between two
+    levels."""
+    from adaptive_top_sparse_quest_b200 import KVCache, quantize_keys
+    N, n = 6000, 2 ** bits - 1
+    g = torch.Generator(device="cuda").manual_seed(3 + bits)
+
+    def uni(*s):
+        return torch.rand(s, generator=g, device="cuda")
+
+    k = torch.randn(N, 4, 32, generator=g, device="cuda") * torch.exp2(15 - 41 * uni(N, 4, 1))
+    step = torch.exp2(torch.floor(-24 + 30 * uni(2000, 4, 1))) * torch.floor(1 + 7 * uni(2000, 4, 1))
+    half = torch.floor(uni(2000, 4, 32) * (2 * n + 1))       # halves of a level
+    half[..., 0], half[..., 1] = 0, 2 * n
+    k[:2000] = half * step / 2 - step * torch.floor(9 * uni(2000, 4, 1))
+    k[4000:4100, 1] = k[4000:4100, 1, :1]                    # all alike
+    k = k.clamp(-65504, 65504).half().view(1, 1, N, D)
+    kv = KVCache(k, None, i32([N]), None, bits)
+    keys = quantize_keys(kv)
+    rc, rs, rz = O.quantize_keys(np16(k), bits)
+    assert (np16(keys.scales).view("u2") == rs.view("u2")).all()
+    assert (np16(keys.zeros).view("u2") == rz.view("u2")).all()
+    assert (np16(keys.codes) == rc).all()
+
+
 def test_write_rows_without_keys_or_meta_and_bad_slots():
     from adaptive_top_sparse_quest_b200 import write_rows
     kv = _cache(2, 2, 4, True, 0, 4)
