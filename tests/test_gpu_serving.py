@@ -623,8 +623,9 @@ def test_long_pool_offsets():
 
 
 def test_write_rows_captured_and_slot_listed_twice():
-    """A captured write replayed with other rows and slots; a slot that is listed
-    twice holds one of its rows, and nothing else changes."""
+    """A captured write replayed with other rows and slots; of a slot that is listed
+    twice the contents are unspecified (two warps store the row, 16 bytes a lane, in
+    any order: each value is one of the two tokens'), and nothing else changes."""
     from adaptive_top_sparse_quest_b200 import write_rows
     kv = _cache(2, 2, 4, True, 0, 4)
     new = torch.randn(4, 2, D, device="cuda").half()
@@ -643,7 +644,7 @@ def test_write_rows_captured_and_slot_listed_twice():
                 want[x // PAGE, :, x % PAGE] = new[i]
         if s[1] == s[2]:
             got = kv.k[1, :, 4]
-            assert all(any(torch.equal(got[h], new[i, h]) for i in (1, 2)) for h in range(2))
+            assert bool(((got == new[1]) | (got == new[2])).all())
             want[1, :, 4] = got
         assert torch.equal(kv.k, want)
 
