@@ -679,12 +679,11 @@ def update_page_table(seq_lens: torch.Tensor, new_lens: torch.Tensor, page_table
     return u(new_lens, num_free, stream)
 
 
-def _token_rows(t: torch.Tensor, name: str, kv: KVCache, T: int) -> int:
+def _token_rows(t: torch.Tensor, name: str, T: int, Hk: int, index: int) -> int:
     """Check new rows [T][Hk][128] (a slice of a wider projection may be given:
     only the last two dimensions must be packed).  Returns the token stride."""
-    Hk = kv.k.shape[1]
-    if t.dtype is not torch.float16 or t.device != kv.k.device or t.shape != (T, Hk, HEAD_DIM):
-        raise ValueError(f"{name} must be fp16 [{T}][{Hk}][128] on {kv.k.device}")
+    if t.dtype is not torch.float16 or t.get_device() != index or t.shape != (T, Hk, HEAD_DIM):
+        raise ValueError(f"{name} must be fp16 [{T}][{Hk}][128] on the cache's device")
     stride, sh, sd = t.stride()
     if sd != 1 or (sh != HEAD_DIM and Hk > 1):
         raise ValueError(f"{name}: a token's heads must lie side by side")
@@ -703,34 +702,50 @@ def write_rows(kv: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: tor
     """Write new K / V rows [T][Hk][128] to the cache slots slots [T] (int32, -1
     skips) and, in the same pass, quantise the keys into `keys` and fold them
     into `meta` (if given): tw_write_rows."""
-    lib = _capi.load()
-    k = kv.k
-    dev = k.device
-    if kv.v is None or kv.v.device != dev:
-        raise ValueError(f"the cache needs a v on {dev}")
-    if not kv.paged and k.shape[0] < kv.B:
-        raise ValueError(f"the cache has {k.shape[0]} sequences, seq_lens {kv.B}")
+    k, v, table = kv.k, kv.v, kv.page_table
+    index = k.get_device()
+    # (a call for single tokens is as long as these lines: each property is read once)
+    def same(t, dtype, shape, name):
+        if (t.dtype is not dtype or t.get_device() != index or t.shape != shape
+                or not t.is_contiguous()):
+            _need_on(t, dtype, name, k.device, shape)
+
+    if v is None or v.get_device() != index:
+        raise ValueError(f"the cache needs a v on {k.device}")
+    pool, Hk, rows, _ = k.shape
+    B = kv.seq_lens.shape[0]
+    if table is None:
+        if pool < B:
+            raise ValueError(f"the cache has {pool} sequences, seq_lens {B}")
+        lead, width, pages = (B, Hk, rows), 0, 0
+    else:
+        lead, width, pages = (pool, Hk, PAGE), table.shape[1], pool
     if slots.dim() != 1:
         raise ValueError("slots must be [T]")
-    if slots.dtype is not torch.int32 or slots.device != dev or not slots.is_contiguous():
-        _need_on(slots, torch.int32, "slots", dev)
     T = slots.shape[0]
-    ks, vs = _token_rows(k_new, "k_new", kv, T), _token_rows(v_new, "v_new", kv, T)
-    codes = scales = zeros = None
+    same(slots, torch.int32, (T,), "slots")
+    k_stride = _token_rows(k_new, "k_new", T, Hk, index)
+    v_stride = _token_rows(v_new, "v_new", T, Hk, index)
+    codes = scales = zeros = mp = None
     if keys is not None:
-        codes, scales, zeros = keys.codes, keys.scales, keys.zeros
-        _check_keys(kv, keys)
-        _need_on(codes, torch.uint8, "codes", dev)
-        groups = kv.row_shape(4)
-        _need_on(scales, torch.float16, "scales", dev, groups)
-        _need_on(zeros, torch.float16, "zeros", dev, groups)
+        c, sc, z = keys.codes, keys.scales, keys.zeros
+        if c.shape != lead + (kv.code_bytes,):
+            _check_keys(kv, keys)
+        same(c, torch.uint8, lead + (kv.code_bytes,), "codes")
+        same(sc, torch.float16, lead + (4,), "scales")
+        same(z, torch.float16, lead + (4,), "zeros")
+        codes, scales, zeros = c.data_ptr(), sc.data_ptr(), z.data_ptr()
     if meta is not None:
-        _need_on(meta, torch.float16, "meta", dev, kv.meta_shape())
+        same(meta, torch.float16, kv.meta_shape(), "meta")
+        mp = meta.data_ptr()
     if T == 0:
         return
-    _launch(lib.tw_write_rows, "tw_write_rows", dev, stream,
-            ctypes.byref(kv.struct()), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-            slots.data_ptr(), T, _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(meta))
+    st = TwKv(k.data_ptr(), v.data_ptr(), B, Hk, width * PAGE if pages else rows,
+              kv.seq_lens.data_ptr(), table.data_ptr() if pages else None, width, pages, PAGE,
+              HEAD_DIM, kv.key_bits)
+    _launch(_capi.load().tw_write_rows, "tw_write_rows", k.device, stream, ctypes.byref(st),
+            k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, slots.data_ptr(), T, codes,
+            scales, zeros, mp)
 
 
 def prefix_workspace_bytes(B: int, Hq: int, Hk: int, prefix_len: int) -> int:
