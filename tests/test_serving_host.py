@@ -60,7 +60,7 @@ WR = dict(kv={}, k=P, ks=256, v=P, vs=256, slots=P, T=3, codes=P, scales=P, zero
     (dict(kv=dict(key_bits=3)), UNS),
     (dict(kv=dict(page_table=P, max_pages_per_seq=4, num_pool_pages=2 ** 27, num_kv_heads=1),
           ks=256), UNS),
-    (dict(T=0), _capi.TW_OK), (dict(kv=dict(batch=0)), _capi.TW_OK),
+    (dict(T=2 ** 30), UNS), (dict(T=0), _capi.TW_OK), (dict(kv=dict(batch=0)), _capi.TW_OK),
 ])
 def test_write_rows_refusals(lib, change, want):
     a = dict(WR, **change)
