@@ -44,6 +44,7 @@
 //   - many short own parts (16 sequences of a multi-head layer): 46, 31 by bytes;
 //   - small calls (15 .. 18): latency: set-up 2, first copies 2, a tile's chain 2,
 //     the records and the join 6.
+#include <algorithm>
 #include <cstring>
 
 #include "tw_common.cuh"
@@ -915,11 +916,13 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
 // Join a row's records: W warps per output row.  A warp's lanes look 32 records
 // up at a time, of those that may be there; the warp then adds them with four
 // channels per lane, four loads in flight; the warps' sums are added in order,
-// so that the result does not depend on timing.  W = 4 where the prefix's
-// records are many (few units, split over many CTAs), else 1.
+// so that the result does not depend on timing.  W = 4 where the prefix's records
+// are many (few units, split over many CTAs) and the rows fewer than eight warps for
+// every SM (168 rows of 16 records: calls of 18.0 us, 20.7 with one warp), else 1
+// (2048 rows of 18: 73.7, 75.4 with four; 96 of 4: 14.9, 15.1).
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinMany = 12;
+constexpr int kJoinMany = 12, kJoinRows = 8 * kPdCtas;
 
 // Output row bh (KV head h) by one warp alone, from sequence 0's first len rows:
 // a key per lane, then four channels per lane.
@@ -1237,11 +1240,13 @@ cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int p
   } else if ((e = cudaMemsetAsync(a.cum, 0, ((size_t)L.B + 1) * sizeof(uint64_t), st)) != cudaSuccess) {
     return e;
   }
-  // records of a row of the prefix: the CTAs that share its unit, two streams each
+  // records of a row of the prefix: the CTAs that share its unit, two streams each,
+  // of a tile at least
   const int64_t S1 = (int64_t)L.Hk * a.RT * a.KT;
-  const int64_t many = S1 > 0 ? (int64_t)a.KT * kPdCtas / S1 * (a.pair ? 1 : 2) : 0;
+  const int64_t many =
+      S1 > 0 ? std::min<int64_t>(a.KT, (int64_t)a.KT * kPdCtas / S1 * (a.pair ? 1 : 2)) : 0;
   const int64_t out_rows = (int64_t)L.B * Hq;
-  if (many >= kJoinMany)
+  if (many >= kJoinMany && out_rows < kJoinRows)
     return launch_k(k_prefix_join<kJoinWarps>, dim3((unsigned)out_rows), dim3(kJoinThreads), 0, st,
                     rows > 0, a);
   return launch_k(k_prefix_join<1>, dim3((unsigned)((out_rows + kJoinWarps - 1) / kJoinWarps)),
