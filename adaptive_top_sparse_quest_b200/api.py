@@ -603,12 +603,38 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _launch(f, where: str, device: torch.device, stream, *args) -> None:
+class _Made:
+    """Orders calls on any stream behind the making of a step's buffers.  A fill
+    of theirs, and work that still uses memory they were given, may be waiting on
+    the stream that was current then: a call on another stream waits for what
+    that stream held, once.  Not while a call is captured (a graph cannot wait
+    for work outside it; torch.cuda.graph synchronises the device first)."""
+    __slots__ = ("event", "ordered")
+
+    def __init__(self, device: torch.device):
+        s = torch.cuda.current_stream(device)
+        self.ordered = {s.cuda_stream}
+        # (made inside a capture: the buffers belong to that graph, and so do its calls)
+        self.event = None if torch.cuda.is_current_stream_capturing() else s.record_event()
+
+    def wait(self, device: torch.device, stream, handle: int) -> None:
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        with torch.cuda.stream(s):
+            if self.event is None or torch.cuda.is_current_stream_capturing():
+                return
+        s.wait_event(self.event)
+        self.ordered.add(handle)
+
+
+def _launch(f, where: str, device: torch.device, stream, *args,
+            made: Optional[_Made] = None) -> None:
     """f(*args, stream) with the tensors' device current; `stream`, or that
     device's current stream."""
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
+    if made is not None and handle not in made.ordered:
+        made.wait(device, stream, handle)
     if torch.cuda.current_device() == device.index:
         status = f(*args, handle)
     else:
@@ -631,7 +657,9 @@ class PageTableUpdate:
     token, -1 where there is none) and offsets [B + 1] (a sequence's first
     place in slots).  in_place: seq_lens and num_free take the results
     themselves (the names above are then the same tensors), so that a captured
-    call can be replayed step after step."""
+    call can be replayed step after step.  Calls may come on any stream, one
+    after another: they share the output buffers, which are to be kept until
+    the last call's work is done."""
 
     def __init__(self, seq_lens: torch.Tensor, page_table: torch.Tensor,
                  free_pages: torch.Tensor, num_slots: int = 0, prefix_len: int = 0,
@@ -649,9 +677,10 @@ class PageTableUpdate:
         self.prefix_len, self.in_place, self.num_slots = int(prefix_len), bool(in_place), int(num_slots)
         with torch.cuda.device(dev):
             self.seq_lens_out = seq_lens if in_place else torch.empty_like(seq_lens)
-            self.num_free_out = None if in_place else seq_lens.new_zeros(1)
-            self.slots = seq_lens.new_full((num_slots,), -1)
-            self.offsets = seq_lens.new_zeros(B + 1)
+            self.num_free_out = None if in_place else seq_lens.new_empty(1)
+            self.slots = seq_lens.new_empty(num_slots)   # every call writes all of them
+            self.offsets = seq_lens.new_empty(B + 1)
+            self._made = _Made(dev)
 
     def __call__(self, new_lens: torch.Tensor, num_free: torch.Tensor,
                  stream=None) -> "PageTableUpdate":
@@ -665,7 +694,8 @@ class PageTableUpdate:
                 B, _ptr(self.seq_lens), _ptr(new_lens), _ptr(self.page_table), W, self.prefix_len,
                 _ptr(self.free_pages), self.free_pages.shape[0], _ptr(num_free),
                 _ptr(self.num_free_out), _ptr(self.seq_lens_out),
-                _ptr(self.slots) if self.num_slots else None, self.num_slots, _ptr(self.offsets))
+                _ptr(self.slots) if self.num_slots else None, self.num_slots, _ptr(self.offsets),
+                made=self._made)
         return self
 
 
@@ -762,7 +792,9 @@ class PrefixDecodeStep:
     [B][Hq][128], `lse` [B][Hq] (or None) and workspace for repeated calls.
 
     The shared tokens are read once, from sequence 0's first pages (or
-    contiguous rows).  prefix_len 0 shares nothing: plain dense decode."""
+    contiguous rows).  prefix_len 0 shares nothing: plain dense decode.  Calls
+    may come on any stream, one after another: they share the outputs and the
+    workspace, which are to be kept until the last call's work is done."""
 
     def __init__(self, kv: KVCache, Hq: int, prefix_len: int, with_lse: bool = True):
         if kv.v is None:
@@ -778,12 +810,13 @@ class PrefixDecodeStep:
             raise ValueError(f"the cache has {shape[0]} sequences, seq_lens {kv.B}")
         self.kv, self.Hq, self.prefix_len = kv, int(Hq), int(prefix_len)
         with torch.cuda.device(dev):
-            self.out = torch.zeros((kv.B, Hq, HEAD_DIM), dtype=torch.float16, device=dev)
-            self.lse = torch.zeros((kv.B, Hq), dtype=torch.float32, device=dev) if with_lse \
+            self.out = torch.empty((kv.B, Hq, HEAD_DIM), dtype=torch.float16, device=dev)
+            self.lse = torch.empty((kv.B, Hq), dtype=torch.float32, device=dev) if with_lse \
                 else None
             n = max(prefix_workspace_bytes(kv.B, self.Hq, kv.Hk, self.prefix_len), 256)
             self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
             self.ws[:256].zero_()   # the device status word
+            self._made = _Made(dev)
         self._kvs = kv.struct()
 
     def __call__(self, q: torch.Tensor, stream=None) -> torch.Tensor:
@@ -793,7 +826,7 @@ class PrefixDecodeStep:
             return self.out
         _launch(lib.tw_prefix_decode, "tw_prefix_decode", self.kv.k.device, stream,
                 _ptr(q), self.Hq, ctypes.byref(self._kvs), self.prefix_len, _ptr(self.out),
-                _ptr(self.lse), _ptr(self.ws), self.ws.numel())
+                _ptr(self.lse), _ptr(self.ws), self.ws.numel(), made=self._made)
         return self.out
 
 

@@ -1,0 +1,109 @@
+"""The serving operators' handles on streams other than the one they were made
+on: what that stream still holds when a handle is made (its buffers' fills, and
+work on memory that the buffers were given) comes before the calls."""
+import pytest
+import torch
+
+from _serving import PAGE, check_attention, make_prefix_case, model_page_table
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from adaptive_top_sparse_quest_b200 import _capi, build
+    build.build()
+    _capi.load()
+    # kernels are loaded at their first use, which may wait for the device: here
+    _backlog(1024)
+    x = torch.zeros(64, dtype=torch.float16, device="cuda")
+    for t in (x, x.float(), x.int()):
+        t.clone()
+    torch.cuda.synchronize()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _backlog(words):
+    """Some 50 ms of work on the current stream, then a fill of memory that is
+    free for the next allocation of `words` 32-bit words."""
+    torch.cuda._sleep(100_000_000)
+    t = torch.full((words,), 0x5A5A5A5A, dtype=torch.int32, device="cuda")
+    del t
+
+
+@pytest.mark.parametrize("passed", [True, False])
+def test_prefix_decode_made_on_a_busy_stream(passed):
+    """`passed`: the other stream is given to the call; else it is current."""
+    from adaptive_top_sparse_quest_b200 import KVCache, PrefixDecodeStep, device_status
+    q, k, v, table, lens = make_prefix_case(12, 8, 2, 32, [50, 32, 0, 300], True)
+    kv = KVCache(k, v, lens, table)
+    PrefixDecodeStep(kv, 8, 32)(q)      # the library is loaded, the memory cached
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _backlog(4 * 8 * 64)                # as large as out
+    step = PrefixDecodeStep(kv, 8, 32)
+    if passed:
+        step(q, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            step(q)
+    with torch.cuda.stream(side):
+        first = step.out.clone(), step.lse.clone()
+    torch.cuda.synchronize()
+    check_attention(q, k, v, table, lens.tolist(), *first)
+    assert device_status(step.ws) == 0
+    assert torch.equal(step.out, first[0]) and torch.equal(step.lse, first[1])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_page_table_made_on_a_busy_stream(in_place):
+    from adaptive_top_sparse_quest_b200 import PageTableUpdate
+    old, new = [0, 20, 33, 5], [40, 21, 0, 5]
+    table = [[-1] * 4, [3, 4, -1, -1], [5, 6, 7, -1], [8, -1, -1, -1]]
+    free = [0, 1, 2] + [9] * 9
+    lens_t, new_t, table_t, free_t, nf_t = i32(old), i32(new), i32(table), i32(free), i32([3])
+    args = (lens_t.clone(), table_t.clone(), free_t.clone(), 50)
+    PageTableUpdate(*args)(new_t, nf_t.clone())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _backlog(50)                        # as large as slots
+    u = PageTableUpdate(lens_t, table_t, free_t, 50, in_place=in_place)
+    u(new_t, nf_t, stream=side)
+    with torch.cuda.stream(side):
+        slots, offsets = u.slots.clone(), u.offsets.clone()
+    torch.cuda.synchronize()
+    want = model_page_table(old, new, table, free, 3, 50, 0)
+    for s, o in ((slots, offsets), (u.slots, u.offsets)):
+        assert s.tolist() == want[2] and o.tolist() == want[3]
+    assert u.seq_lens_out.tolist() == want[0] and int(u.num_free_out) == want[1]
+    assert table_t.tolist() == table and free_t.tolist() == free
+
+
+def test_handles_made_before_or_inside_a_capture():
+    """A step made outside is captured on the graph's own stream; one made inside
+    belongs to the graph."""
+    from adaptive_top_sparse_quest_b200 import (KVCache, PageTableUpdate, PrefixDecodeStep,
+                                                prefix_decode)
+    q, k, v, table, lens = make_prefix_case(13, 8, 2, 32, [70, 33, 100], True)
+    kv = KVCache(k, v, lens, table)
+    step = PrefixDecodeStep(kv, 8, 32)
+    old, new, nf = i32([0, 3]), i32([17, 4]), i32([5])
+    pt, free = i32([[-1] * 2, [6, -1]]), i32([0, 1, 2, 3, 4, 0, 0])
+    u = PageTableUpdate(old, pt, free, 20)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(q)
+        out, lse = prefix_decode(q, kv, 32)
+        u(new, nf)
+    g.replay()
+    torch.cuda.synchronize()
+    check_attention(q, k, v, table, lens.tolist(), step.out, step.lse)
+    assert torch.equal(out, step.out) and torch.equal(lse, step.lse)
+    want = model_page_table([0, 3], [17, 4], [[-1] * 2, [6, -1]], [0, 1, 2, 3, 4, 0, 0], 5, 20, 0)
+    assert u.slots.tolist() == want[2] and u.seq_lens_out.tolist() == want[0]
+    assert PAGE * (pt.shape[1]) >= max(want[0])
