@@ -792,23 +792,15 @@ class PrefixDecodeStep:
     [B][Hq][128], `lse` [B][Hq] (or None) and workspace for repeated calls.
 
     The shared tokens are read once, from sequence 0's first pages (or
-    contiguous rows).  prefix_len 0 shares nothing: plain dense decode.  Calls
+    contiguous rows).  prefix_len 0 shares nothing: plain dense decode.  A call
+    reads the tensors that kv names then; their batch and heads stay.  Calls
     may come on any stream, one after another: they share the outputs and the
     workspace, which are to be kept until the last call's work is done."""
 
     def __init__(self, kv: KVCache, Hq: int, prefix_len: int, with_lse: bool = True):
-        if kv.v is None:
-            raise ValueError("the cache has no v")
-        if prefix_len < 0 or prefix_len % PAGE or prefix_len > kv.N:
-            raise ValueError(f"prefix_len must be a multiple of {PAGE} in [0, {kv.N}]")
-        dev = kv.k.device
-        for t, name in ((kv.v, "v"), (kv.seq_lens, "seq_lens"), (kv.page_table, "page_table")):
-            if t is not None and t.device != dev:
-                raise ValueError(f"{name} must be on {dev}, got {t.device}")
-        shape = (kv.page_table if kv.paged else kv.k).shape
-        if shape[0] != kv.B:
-            raise ValueError(f"the cache has {shape[0]} sequences, seq_lens {kv.B}")
         self.kv, self.Hq, self.prefix_len = kv, int(Hq), int(prefix_len)
+        dev = kv.k.device
+        self._bind()
         with torch.cuda.device(dev):
             self.out = torch.empty((kv.B, Hq, HEAD_DIM), dtype=torch.float16, device=dev)
             self.lse = torch.empty((kv.B, Hq), dtype=torch.float32, device=dev) if with_lse \
@@ -817,10 +809,35 @@ class PrefixDecodeStep:
             self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
             self.ws[:256].zero_()   # the device status word
             self._made = _Made(dev)
-        self._kvs = kv.struct()
+        self._shape = kv.B, kv.Hk, dev
+
+    def _bind(self) -> None:
+        """Check the cache's present tensors and take their addresses."""
+        kv = self.kv
+        kv.__post_init__()
+        if kv.v is None:
+            raise ValueError("the cache has no v")
+        if self.prefix_len < 0 or self.prefix_len % PAGE or self.prefix_len > kv.N:
+            raise ValueError(f"prefix_len must be a multiple of {PAGE} in [0, {kv.N}]")
+        dev = kv.k.device
+        for t, name in ((kv.v, "v"), (kv.seq_lens, "seq_lens"), (kv.page_table, "page_table")):
+            if t is not None and t.device != dev:
+                raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        shape = (kv.page_table if kv.paged else kv.k).shape
+        if shape[0] != kv.B:
+            raise ValueError(f"the cache has {shape[0]} sequences, seq_lens {kv.B}")
+        self._kvs, self._bound = kv.struct(), (kv.k, kv.v, kv.seq_lens, kv.page_table)
 
     def __call__(self, q: torch.Tensor, stream=None) -> torch.Tensor:
         lib = _capi.load()
+        kv, (k, v, lens, table) = self.kv, self._bound
+        if (kv.k is not k or kv.v is not v or kv.seq_lens is not lens
+                or kv.page_table is not table):   # the cache has other tensors by now
+            if (kv.B, kv.Hk, kv.k.device) != self._shape:
+                raise ValueError("the step was made for [B, Hk, device] = "
+                                 f"{list(self._shape)}, the cache is "
+                                 f"{[kv.B, kv.Hk, kv.k.device]}")
+            self._bind()
         _need_on(q, torch.float16, "q", self.kv.k.device, (self.kv.B, self.Hq, HEAD_DIM))
         if self.kv.B == 0:
             return self.out

@@ -107,3 +107,37 @@ def test_handles_made_before_or_inside_a_capture():
     want = model_page_table([0, 3], [17, 4], [[-1] * 2, [6, -1]], [0, 1, 2, 3, 4, 0, 0], 5, 20, 0)
     assert u.slots.tolist() == want[2] and u.seq_lens_out.tolist() == want[0]
     assert PAGE * (pt.shape[1]) >= max(want[0])
+
+
+def test_prefix_decode_after_the_cache_changed_its_tensors():
+    """A step reads the tensors that its cache names at the call: lengths that an
+    update returned in a tensor of its own, a wider table, a pool that moved.
+    Tensors that do not fit the step are refused."""
+    from adaptive_top_sparse_quest_b200 import KVCache, PrefixDecodeStep, device_status
+    q, k, v, table, lens = make_prefix_case(14, 8, 2, 32, [200, 140, 90], True)
+    kv = KVCache(k, v, lens, table)
+    step = PrefixDecodeStep(kv, 8, 32)
+    step(q)
+    check_attention(q, k, v, table, [200, 140, 90], step.out, step.lse)
+    kv.seq_lens = i32([33, 0, 88])
+    step(q)
+    check_attention(q, k, v, table, [33, 0, 88], step.out, step.lse)
+    kv.page_table = torch.cat([table, table.new_full((3, 3), -1)], 1)
+    kv.k, kv.v = (torch.cat([x[:1], x]) for x in (k, v))
+    kv.page_table = kv.page_table + 1
+    kv.seq_lens = i32([199, 1, 60])
+    step(q)
+    check_attention(q, kv.k, kv.v, kv.page_table, [199, 1, 60], step.out, step.lse)
+    assert device_status(step.ws) == 0
+    good = kv.k, kv.v, kv.seq_lens, kv.page_table
+    for change in (dict(seq_lens=lens[:2].contiguous()), dict(v=None), dict(v=kv.v[1:]),
+                   dict(page_table=table[:2].contiguous()), dict(seq_lens=lens.cpu()),
+                   dict(page_table=table[:, :1].contiguous()), dict(k=kv.k[:, :1].contiguous())):
+        kv.k, kv.v, kv.seq_lens, kv.page_table = good
+        for name, t in change.items():
+            setattr(kv, name, t)
+        with pytest.raises(ValueError):
+            step(q)
+    kv.k, kv.v, kv.seq_lens, kv.page_table = good
+    step(q)
+    check_attention(q, kv.k, kv.v, kv.page_table, [199, 1, 60], step.out, step.lse)
