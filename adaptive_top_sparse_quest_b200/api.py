@@ -76,6 +76,14 @@ class KVCache:
             raise ValueError("contiguous k must be [B][Hk][N][128]")
         if self.key_bits not in KEY_BITS:
             raise ValueError(f"key_bits must be one of {KEY_BITS}")
+        self._checked = self.k, self.v, self.seq_lens, self.page_table
+
+    def recheck(self) -> None:
+        """Check the tensors again if some have been replaced since."""
+        k, v, lens, table = self._checked
+        if (self.k is not k or self.v is not v or self.seq_lens is not lens
+                or self.page_table is not table):
+            self.__post_init__()
 
     @property
     def code_bytes(self) -> int:
@@ -732,6 +740,7 @@ def write_rows(kv: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: tor
     """Write new K / V rows [T][Hk][128] to the cache slots slots [T] (int32, -1
     skips) and, in the same pass, quantise the keys into `keys` and fold them
     into `meta` (if given): tw_write_rows."""
+    kv.recheck()
     k, v, table = kv.k, kv.v, kv.page_table
     index = k.get_device()
     # (a call for single tokens is as long as these lines: each property is read once)
@@ -814,7 +823,7 @@ class PrefixDecodeStep:
     def _bind(self) -> None:
         """Check the cache's present tensors and take their addresses."""
         kv = self.kv
-        kv.__post_init__()
+        kv.recheck()
         if kv.v is None:
             raise ValueError("the cache has no v")
         if self.prefix_len < 0 or self.prefix_len % PAGE or self.prefix_len > kv.N:

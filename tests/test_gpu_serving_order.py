@@ -141,3 +141,25 @@ def test_prefix_decode_after_the_cache_changed_its_tensors():
     kv.k, kv.v, kv.seq_lens, kv.page_table = good
     step(q)
     check_attention(q, kv.k, kv.v, kv.page_table, [199, 1, 60], step.out, step.lse)
+
+
+def test_write_rows_after_the_cache_changed_its_tensors():
+    """A call writes to the tensors that the cache names then, and refuses those
+    that do not go together."""
+    from adaptive_top_sparse_quest_b200 import KVCache, write_rows
+    k = torch.zeros(6, 2, PAGE, 128, dtype=torch.float16, device="cuda")
+    kv = KVCache(k, k.clone(), i32([0]), i32([[1, 2]]))
+    new, slots = torch.randn(2, 2, 128, device="cuda").half(), i32([18, 100])
+    for bad in (k[:3], k.float(), k[..., :64], k.transpose(0, 1), None):
+        kv.v = bad
+        with pytest.raises((ValueError, TypeError)):
+            write_rows(kv, new, new, slots)
+    kv.k, kv.v = torch.zeros_like(k), torch.zeros_like(k)
+    write_rows(kv, new, new, slots)
+    want = torch.zeros_like(k)
+    want[1, :, 2] = new[0]              # slot 100 lies outside this pool of 96
+    assert torch.equal(kv.k, want) and torch.equal(kv.v, want)
+    kv.k, kv.v = torch.zeros_like(k).repeat(2, 1, 1, 1), torch.zeros_like(k).repeat(2, 1, 1, 1)
+    write_rows(kv, new, new, slots)
+    assert torch.equal(kv.k[1, :, 2], new[0]) and torch.equal(kv.v[6, :, 4], new[1])
+    assert not bool(k.any())
