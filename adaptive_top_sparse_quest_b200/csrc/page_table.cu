@@ -33,6 +33,18 @@ namespace tw {
 constexpr int kPtThreads = 1024;
 constexpr int kPtPer = kPtMaxBatch / kPtThreads;   // sequences per thread in the scans
 
+// Pages that a stack of `height` (at most cap) takes of `give`.  The sum of the
+// two may pass 32 bits: up to 2^31 - 1 table entries, 2^27 pages of a pool.
+__host__ __device__ constexpr int pushed(int height, int give, int cap) {
+  return give < cap - height ? give : cap - height;
+}
+constexpr int kPtMaxPool = INT32_MAX / kPage;
+static_assert(pushed(kPtMaxPool, INT32_MAX, kPtMaxPool) == 0, "full stack");
+static_assert(pushed(1, INT32_MAX, kPtMaxPool) == kPtMaxPool - 1, "32-bit sums");
+static_assert(pushed(0, 7, 8) == 7 && pushed(3, 7, 8) == 5 && pushed(3, 0, 8) == 0, "stack room");
+// strides of the loops over them stay in range as well
+static_assert(kPtMaxPool <= INT32_MAX - 16 * kPtThreads, "loop index");
+
 struct PtSmem {
   int64_t scan64[32];
   int scan32[32];
@@ -152,15 +164,14 @@ __global__ void __launch_bounds__(kPtThreads) k_update_page_table(PtArgs a) {
     }
   }
   __syncthreads();
-  // pages given back, in order of sequence and page, onto the stack (a stack
-  // that would pass its capacity, which only a page held twice can cause,
-  // drops what does not fit)
-  const int avail = min(F + give_all, a.cap);
-  for (int i = gt; i < give_all; i += nt) {
+  // pages given back, in order of sequence and page, onto the stack; what would
+  // pass its capacity, which only a page held twice or a length above the real one
+  // can cause, is dropped
+  const int given = pushed(F, give_all, a.cap), avail = F + given;
+  for (int i = gt; i < given; i += nt) {
     const int b = upper(give_end, a.B, i);
     const int at = i - (b ? give_end[b - 1] : 0);
-    if (F + i < a.cap)
-      a.free_pages[F + i] = a.page_table[(int64_t)b * a.W + pages(new_len[b]) + at];
+    a.free_pages[F + i] = a.page_table[(int64_t)b * a.W + pages(new_len[b]) + at];
   }
   if (cluster_size() > 1)
     cluster_sync();

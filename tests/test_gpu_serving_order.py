@@ -163,3 +163,26 @@ def test_write_rows_after_the_cache_changed_its_tensors():
     write_rows(kv, new, new, slots)
     assert torch.equal(kv.k[1, :, 2], new[0]) and torch.equal(kv.v[6, :, 4], new[1])
     assert not bool(k.any())
+
+
+def test_page_table_sums_past_32_bits():
+    """Lengths far above the real ones in the largest table: what is given back and
+    the stack's height together pass 2^31, and the stack takes what it has room for."""
+    from adaptive_top_sparse_quest_b200 import update_page_table
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    B, W, pool, height = 8192, 262143, 400000, 300000
+    table = torch.full((B, W), -1, dtype=torch.int32, device="cuda")
+    table[0] = torch.arange(W, dtype=torch.int32, device="cuda")
+    free = torch.arange(pool, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    before = free.clone()
+    old, new = i32([2 ** 31 - 1] * (B - 1) + [0]), i32([0] * (B - 1) + [20])
+    u = update_page_table(old, new, table, free, i32([height]), num_slots=24)
+    n = pool - height
+    assert int(u.num_free_out) == pool - 2
+    assert torch.equal(free[:height], before[:height])
+    assert torch.equal(free[height:], table[0, :n])
+    assert table[-1, :3].tolist() == [n - 1, n - 2, -1]
+    slots = [(n - 1 - t // PAGE) * PAGE + t % PAGE for t in range(20)]
+    assert u.slots.tolist() == slots + [-1] * 4
+    assert u.seq_lens_out.tolist() == new.tolist() and u.offsets.tolist() == [0] * B + [20]
