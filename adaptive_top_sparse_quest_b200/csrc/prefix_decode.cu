@@ -9,9 +9,9 @@
 // so the shared part is read once per 256 query rows instead of once per
 // sequence; a sequence's own tokens meet its G rows the same way.  A softmax
 // over any subset of the keys is summed up by (m, l = sum P, O); subsets are
-// joined by weights 2^(m_i - m).  Each CTA takes an equal share of the key tiles
-// (128 keys), writes a record (m, l, O) per row and unit it touched, and a second
-// kernel joins a row's records.
+// joined by weights 2^(m_i - m).  Each CTA takes a stretch of the list of key
+// tiles (128 keys) that costs as much as any other's, writes a record (m, l, O)
+// per row and unit it touched, and a second kernel joins a row's records.
 //
 // Pipeline.  One CTA per SM, twelve warps, two streams of tiles:
 //   - a warp per stream copies its query rows, and K and V (page by page, 16 rows
@@ -580,9 +580,14 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         if (last) umma_commit(&c.qempty[i]);
         ok = mbar_wait(&c.vfull[i], j & 1, a.status);
         if (!ok) break;
-        if (valid & (kPage - 1)) {
-          // rows past the sequence's end meet weights of zero, whatever they
-          // hold: make them zero
+        if (!thin) {
+          ok = mbar_wait(&c.phalf[i], nt & 1, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_o(i, i, np, more, 0);
+        } else if (valid & (kPage - 1)) {
+          // rows past a sequence's end meet weights of zero, whatever they hold:
+          // make them zero (the prefix ends with a page)
           const int nz = (int)np * kPage - valid;
           for (int y = lane; y < nz * 16; y += 32) {
             const uint32_t at = v_buf(i) + (y & 1) * kBlk + (valid + (y >> 4)) * 128 +
@@ -591,12 +596,6 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
           }
           fence_async_proxy();
           __syncwarp();
-        }
-        if (!thin) {
-          ok = mbar_wait(&c.phalf[i], nt & 1, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          issue_o(i, i, np, more, 0);
         }
         ok = mbar_wait(&c.pfull[i], nt & 1, a.status);
         if (!ok) break;
@@ -746,8 +745,8 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       }
       const int rows = seg_rows(a, g, i);
       const bool busy = (warp & 3) * 32 < rows;   // this warp has rows
-      int lim = g.keys;                            // keys this row sees
-      if (g.prefix && r < rows) lim = min(lim, a.L.len((first_row(a, g, i) + r) / a.G));
+      int lim = g.keys;                            // keys this row sees (of the prefix)
+      if (r < rows) lim = min(lim, a.L.len((first_row(a, g, i) + r) / a.G));
       float m = kNone, l = 0.f;
       // raise the running maximum (log2 units) to the tile's; past kSlack, or
       // on the first tile, it is taken over and what is summed so far rescaled
@@ -872,13 +871,12 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       ++nseg;
       tc_fence_after();
       if (busy) {
-        const int per = g.prefix ? a.rows1 : a.G;
-        const int64_t at = g.slot * per + (g.prefix && a.pair ? i * kTile : 0);
-        if (r < rows) (g.prefix ? a.ml1 : a.ml2)[at + r] = make_float2(record_max(m), l);
+        const int64_t at = g.slot * a.rows1 + (a.pair ? i * kTile : 0);
+        if (r < rows) a.ml1[at + r] = make_float2(record_max(m), l);
         // 32 columns of the warp's rows at a time, through shared memory, so that
         // eight lanes write 128 bytes of one row
         const int row0 = (warp & 3) * 32, nrow = min(32, rows - row0);
-        float* o_dst = (g.prefix ? a.o1 : a.o2) + (at + row0) * kHeadDim;
+        float* o_dst = a.o1 + (at + row0) * kHeadDim;
         const uint32_t stage = base + 6 * kBuf + warp * kStage;
 #pragma unroll 1
         for (int y = 0; y < 4; ++y) {
