@@ -126,6 +126,7 @@ struct PdThin {
   float x[4][kThin];     // a value per warp and row: maxima, at the end sums
   float m[kThin];
   int lim[kThin];        // keys a row sees
+  int b;                 // sequence of an own part
 };
 
 struct PdCtl {
@@ -179,6 +180,10 @@ __device__ __forceinline__ int prefix_tile_at(const PdArgs& a, int64_t x) {
   return (int)(u * a.KT) + (in <= 0 ? 0 : (in + cost - 1) / cost);
 }
 
+// A value that is the same in all lanes, in a form that lets the compiler know:
+// it then keeps operand descriptors in uniform registers.
+__device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // A run of consecutive key tiles of one unit, on one stream.
 struct Seg {
   bool prefix;
@@ -215,29 +220,37 @@ struct SegIter {
       p += g.n;
       return true;
     }
-    if (s < se) {
-      // tiles are left, so a sequence with some follows (unless the lengths
-      // were changed under the kernel, which ends the list here)
-      while (b < a.L.B - 1 && own_tiles(a, b) == 0) ++b;
-      const int kt = own_tiles(a, b);
-      if (kt <= t) return false;
-      g.prefix = false;
-      g.b = b;
-      g.h = h;
-      g.rt = 0;
-      g.t0 = t;
-      g.n = min(se - s, kt - t);
-      g.keys = a.L.len(b) - a.P;
-      g.slot = (int64_t)2 * blockIdx.x + i + (int64_t)b * a.L.Hk + h;
-      s += g.n;
-      t = 0;
-      if (++h == a.L.Hk) {
-        h = 0;
-        ++b;
-      }
-      return true;
+    return s < se && take(a, i, find(a), g);
+  }
+  // Keys of the next own sequence that has some (0: none is left, although tiles
+  // are: the lengths were changed under the kernel, which ends the list).
+  __device__ __forceinline__ int find(const PdArgs& a) {
+    for (; b < a.L.B; ++b) {
+      const int keys = (int)uni(a.L.len(b)) - a.P;
+      if (keys > 0) return keys;
     }
-    return false;
+    return 0;
+  }
+  // Its tiles from here.  They follow from that one reading of its length, so that a
+  // segment's tiles and keys agree whatever happens to it.
+  __device__ __forceinline__ bool take(const PdArgs& a, int i, int keys, Seg& g) {
+    const int kt = (keys + kTile - 1) / kTile;
+    if (kt <= t) return false;
+    g.prefix = false;
+    g.b = b;
+    g.h = h;
+    g.rt = 0;
+    g.t0 = t;
+    g.n = min(se - s, kt - t);
+    g.keys = keys;
+    g.slot = (int64_t)2 * blockIdx.x + i + (int64_t)b * a.L.Hk + h;
+    s += g.n;
+    t = 0;
+    if (++h == a.L.Hk) {
+      h = 0;
+      ++b;
+    }
+    return true;
   }
 };
 
@@ -266,10 +279,6 @@ __device__ __forceinline__ bool is_thin(const PdArgs& a, const Seg& g) {
 
 // A record's maximum, of the weights without their lift; minus infinity: no record.
 __device__ __forceinline__ float record_max(float m) { return m == kNone ? -INFINITY : m - kLift; }
-
-// A value that is the same in all lanes, in a form that lets the compiler know:
-// it then keeps operand descriptors in uniform registers.
-__device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __global__ void __launch_bounds__(kPdThreads, 1)
 k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -347,6 +356,7 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       r.pm = a.pair ? r.p1 : prefix_tile_at(a, min(xm, X1));
       r.s0 = r.sm = r.s1 = (int)(uint32_t)total * a.L.Hk;   // past the last, unless found below
       c.range = r;
+      for (int k = 0; k < 2; ++k) c.at_b[k] = c.at_h[k] = c.at_t[k] = 0;
     }
     __syncthreads();
     uint64_t before = 0;
@@ -624,22 +634,38 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     Seg g;
     int nt = 0, nseg = 0;
     bool ok = true;
-    // next segment with rows on this stream
-    auto next = [&](Seg& s) {
-      while (it.next(a, i, s))
-        if (seg_rows(a, s, i) > 0) return true;
-      return false;
-    };
     // a thin segment: thread `key` holds that key's scores (then that channel's O) of
     // all rows, every thread the rows' maxima and its share of their sums
     const int w4 = warp & 3, key = r, meet = 1 + i;   // hardware barrier of the four warps
     PdThin& th = c.thin[i];
+    // Next segment with rows on this stream; a thin one's limits.  The four warps meet
+    // at barriers in a thin segment, so they have to agree on it whatever happens to
+    // the lengths in memory: one of them reads them for all.
+    auto next = [&](Seg& s) {
+      while (it.p < it.pe) {
+        it.next(a, i, s);
+        const int rows = seg_rows(a, s, i);
+        if (rows == 0) continue;
+        if (is_thin(a, s)) {
+          if (w4 == 0 && lane < kThin)
+            th.lim[lane] = lane < rows ? min(s.keys, a.L.len(lane / a.G)) : s.keys;
+          bar_sync(meet, 128);
+        }
+        return true;
+      }
+      if (it.s >= it.se) return false;
+      if (w4 == 0) {
+        const int keys = it.find(a);
+        if (lane < kThin) th.lim[lane] = keys;
+        if (lane == 0) th.b = it.b;
+      }
+      bar_sync(meet, 128);   // and P's memory is free of earlier records
+      it.b = th.b;
+      return it.take(a, i, th.lim[0], s);
+    };
     auto thin_seg = [&]() {
       constexpr int NR = kThin;
       const int rows = seg_rows(a, g, i);
-      if (w4 == 0 && lane < NR)
-        th.lim[lane] = g.prefix && lane < rows ? min(g.keys, a.L.len(lane / a.G)) : g.keys;
-      bar_sync(meet, 128);   // and P's memory is free of earlier records
       int low = g.keys;      // keys that every row sees
       float m[NR], l[NR];
 #pragma unroll

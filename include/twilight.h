@@ -442,8 +442,11 @@ int tw_write_rows(const tw_kv* kv, const uint16_t* k_new, int64_t k_stride,
  * and lse = -inf.  Rows at and past a sequence's end do not reach its result,
  * whatever they hold (NaN included; infinite or NaN values in the prefix past the
  * end of a shorter sequence cost that one a slow pass of its own).  A score of
- * NaN or +inf makes a row NaN; scores of -inf count nothing.  Cache rows must number below 2^31.  Workspace:
- * tw_prefix_workspace_size bytes.
+ * NaN or +inf makes a row NaN; scores of -inf count nothing.  Cache rows must
+ * number below 2^31.  seq_lens and page_table are not to change while the call
+ * runs: its results then mean nothing (and the status word may say so), but it
+ * comes to an end and touches nothing outside the arrays.  Workspace:
+ * tw_prefix_workspace_size bytes, for one call at a time.
  */
 int tw_prefix_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                              int32_t prefix_len, size_t* bytes);
