@@ -31,7 +31,9 @@
  *   - fp16 data is passed as uint16_t (IEEE binary16 bit patterns).
  *   - head_dim must be 128 and page_size 16 (TW_ERR_UNSUPPORTED otherwise);
  *     the device must be compute capability 10.0 (sm_100a).
- *   - Inputs must be finite; NaN or Inf in q, K or V gives unspecified results.
+ *   - Inputs must be finite; NaN or Inf in q, K or V gives unspecified results,
+ *     unless a call says otherwise (tw_quantize_keys, tw_append_keys,
+ *     tw_write_rows, tw_prefix_decode).
  *
  * Layouts (element = fp16 unless stated; b = sequence, h = KV head,
  * t = token, pg = logical page = t / 16, N = max_seq_len)
@@ -125,7 +127,8 @@ int tw_version(void);
  * n = 15 (kv->key_bits 4) or 3 (kv->key_bits 2):
  *   mn, mx = exact fp16 min / max (totalOrder: -0 < +0)
  *   scale = fp16_rn((mx - mn) / n),  zero = mn,
- *   code  = clamp(round_half_even((x - mn) / scale), 0, n), 0 if scale == 0.
+ *   code  = clamp(round_half_even((x - mn) / scale), 0, n), 0 if scale == 0
+ *           or not finite (a group with an infinite or NaN key).
  * codes are packed as "Layouts" states for the width.
  * Reads kv->k for tokens t < seq_lens[b]; writes codes/scales/zeros at the same
  * positions (other positions are left untouched).  Bit-exact with the CPU
