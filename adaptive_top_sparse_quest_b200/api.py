@@ -25,6 +25,7 @@ from ._capi import TwKv, TwStep, check
 
 HEAD_DIM = 128
 PAGE = 16
+INT32_MAX = 2 ** 31 - 1
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -679,8 +680,12 @@ class PageTableUpdate:
         B = int(seq_lens.shape[0])
         _need_on(page_table, torch.int32, "page_table", dev, (B, page_table.shape[1]))
         _need_on(free_pages, torch.int32, "free_pages", dev)
-        if num_slots < 0:
-            raise ValueError("num_slots must not be negative")
+        room = PAGE * int(page_table.shape[1])
+        if not 0 <= num_slots <= INT32_MAX or free_pages.shape[0] > INT32_MAX:
+            raise ValueError("num_slots and the pages of the pool must be 32-bit numbers, not "
+                             f"{num_slots} and {free_pages.shape[0]}")
+        if prefix_len < 0 or prefix_len % PAGE or prefix_len > room:
+            raise ValueError(f"prefix_len must be a multiple of {PAGE} in [0, {room}]")
         self.seq_lens, self.page_table, self.free_pages = seq_lens, page_table, free_pages
         self.prefix_len, self.in_place, self.num_slots = int(prefix_len), bool(in_place), int(num_slots)
         with torch.cuda.device(dev):
@@ -789,6 +794,8 @@ def write_rows(kv: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: tor
 
 def prefix_workspace_bytes(B: int, Hq: int, Hk: int, prefix_len: int) -> int:
     lib = _capi.load()
+    if max(B, Hq, Hk, prefix_len) > INT32_MAX:
+        raise ValueError("sizes must be 32-bit numbers")
     n = ctypes.c_size_t(0)
     check(lib.tw_prefix_workspace_size(B, Hq, Hk, prefix_len, ctypes.byref(n)),
           "tw_prefix_workspace_size")

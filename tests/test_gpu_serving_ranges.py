@@ -146,3 +146,16 @@ def test_page_bounds_of_pages_that_change_hands():
                         assert (got[j].view("u2") == full[j].view("u2")).all(), (step, b, h, j)
                         exact += 1
     assert moved > 20 and exact > 500 and wide > 20, (moved, exact, wide)
+
+
+def test_sizes_past_32_bits_and_bad_prefixes_are_refused():
+    """Not cut to their low 32 bits on the way into the library."""
+    from adaptive_top_sparse_quest_b200 import PageTableUpdate, update_page_table
+    lens, table, free = i32([0, 3]), i32([[0, 0], [1, 0]]), i32([2, 3, 4, 0, 0])
+    for bad in (dict(num_slots=-1), dict(num_slots=2 ** 32 + 8), dict(prefix_len=2 ** 32),
+                dict(prefix_len=-16), dict(prefix_len=8), dict(prefix_len=48)):
+        with pytest.raises(ValueError):
+            PageTableUpdate(lens, table, free, **bad)
+        with pytest.raises(ValueError):
+            update_page_table(lens, lens, table, free, i32([3]), **bad)
+    PageTableUpdate(lens, table, free, 8, 32)(lens, i32([3]))
