@@ -44,7 +44,6 @@
 //   - many short own parts (16 sequences of a multi-head layer): 46, 31 by bytes;
 //   - small calls (15 .. 18): latency: set-up 2, first copies 2, a tile's chain 2,
 //     the records and the join 6.
-#include <algorithm>
 #include <cstring>
 
 #include "tw_common.cuh"
@@ -160,8 +159,8 @@ __device__ __forceinline__ int own_tiles(const PdArgs& a, int b) {
 // as long again.  (64 sequences behind 32k tokens: 59 us, 68 with every tile
 // alike; 16 of a multi-head layer, many short units: 41 us, 47 without starts.)
 constexpr int kOwnCost = 6, kOwnStart = 2, kUnitStart = 12;
-__device__ __forceinline__ int tile_cost(const PdArgs& a) { return a.pair ? 9 : 6; }
-__device__ __forceinline__ int unit_span(const PdArgs& a) {
+__host__ __device__ __forceinline__ int tile_cost(const PdArgs& a) { return a.pair ? 9 : 6; }
+__host__ __device__ __forceinline__ int unit_span(const PdArgs& a) {
   return a.KT * tile_cost(a) + kUnitStart;
 }
 __device__ __forceinline__ int64_t prefix_span(const PdArgs& a) {
@@ -940,13 +939,19 @@ k_prefix_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant
 // Join a row's records: W warps per output row.  A warp's lanes look 32 records
 // up at a time, of those that may be there; the warp then adds them with four
 // channels per lane, four loads in flight; the warps' sums are added in order,
-// so that the result does not depend on timing.  W = 4 where the prefix's records
-// are many (few units, split over many CTAs) and the rows fewer than eight warps for
-// every SM (168 rows of 16 records: calls of 18.0 us, 20.7 with one warp), else 1
-// (2048 rows of 18: 73.7, 75.4 with four; 96 of 4: 14.9, 15.1).
+// so that the result does not depend on timing.  W = 4 where a row of the prefix has
+// many records, or so many CTAs share its unit that one warp would look them up in
+// two turns or more, unless rows are many; else 1, since four are four times the
+// warps.  Calls with one warp and with four, in us (medians of ten; 100 shapes), by
+// (places looked up, records of them, rows):
+//   four: (147, 147, 4) 60.4, 37.4; (112, 112, 132) 45.9, 27.4; (81, 1, 48) 16.3, 14.0;
+//         (34, 10, 240) 17.3, 16.2; (32, 32, 1024) 50.5, 44.0; (16, 16, 1280) 50.1, 48.5;
+//         (15, 15, 1088) 22.8, 21.8; (21, 12, 128) 17.4, 17.0
+//   one:  (15, 15, 2048), own parts of 1000 tokens among them, 64.6, 66.0; (12, 12, 1056)
+//         24.8, 25.1; (18, 8, 128) 15.8, 16.1; (16, 3, 80) 13.7, 14.9; (6, 6, 4096) 38.8, 42.2
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinMany = 12, kJoinRows = 8 * kPdCtas;
+constexpr int kJoinMany = 12, kJoinRows = 12 * kPdCtas;
 
 // Output row bh (KV head h) by one warp alone, from sequence 0's first len rows:
 // a key per lane, then four channels per lane.
@@ -1264,13 +1269,14 @@ cudaError_t launch_prefix_decode(const Layout& L, const __half* q, int Hq, int p
   } else if ((e = cudaMemsetAsync(a.cum, 0, ((size_t)L.B + 1) * sizeof(uint64_t), st)) != cudaSuccess) {
     return e;
   }
-  // records of a row of the prefix: the CTAs that share its unit, two streams each,
-  // of a tile at least
-  const int64_t S1 = (int64_t)L.Hk * a.RT * a.KT;
-  const int64_t many =
-      S1 > 0 ? std::min<int64_t>(a.KT, (int64_t)a.KT * kPdCtas / S1 * (a.pair ? 1 : 2)) : 0;
+  // Places that may hold records of a prefix unit: its stretch of the line of costs,
+  // on which every sequence has a tile of its own for each head at least (the lengths
+  // are not known here), in CTAs of one or two; records: a tile each at least
+  const int64_t units = (int64_t)L.Hk * a.RT, span = unit_span(a);
+  const int64_t line = units * span + (int64_t)L.B * L.Hk * (kOwnStart + kOwnCost);
+  const int64_t places = a.KT > 0 ? kPdCtas * (a.pair ? 1 : 2) * span / line : 0;
   const int64_t out_rows = (int64_t)L.B * Hq;
-  if (many >= kJoinMany && out_rows < kJoinRows)
+  if (out_rows < kJoinRows && (places >= 32 || (places >= kJoinMany && a.KT >= kJoinMany)))
     return launch_k(k_prefix_join<kJoinWarps>, dim3((unsigned)out_rows), dim3(kJoinThreads), 0, st,
                     rows > 0, a);
   return launch_k(k_prefix_join<1>, dim3((unsigned)((out_rows + kJoinWarps - 1) / kJoinWarps)),
