@@ -213,10 +213,12 @@ k_append_keys(Layout L, const __half* __restrict__ K, uint8_t* __restrict__ code
 // 15 places further on; it needs no other warp, so a block is only what shares a
 // launch slot.
 //
-// What bounds it (4 bits, one B200): the instructions of the quantiser, 0.6 of the
-// issue slots while rows are there, and latency around them.  8191 tokens x 8
-// heads: 19.3 us (11 by the bytes at the copy rate); 20000 x 32 at 2 bits: 121 (108);
-// 64 single tokens x 8 heads: 2.8, one chain of loads.
+// What bounds it (one B200).  8191 tokens x 8 heads at 4 bits, 19.3 us (11 by the bytes
+// at the copy rate): no unit is full (issue slots 0.6, DRAM a quarter); the grid is one
+// wave, and each warp takes its page in four turns of loads, quantiser and stores that
+// wait for one another.  20000 x 32 at 2 bits, 119 us (108): HBM, 0.9 of the copy rate.
+// 64 single tokens x 8 heads, 2.8 us: one chain of loads.  Many runs of one to three
+// tokens: up to sixteen of those chains in a warp, one after another.
 constexpr int kWrThreads = 128;
 constexpr int kWrWarps = kWrThreads / 32;
 constexpr int kWrRows = 2;   // rows of a run in flight per half-warp

@@ -21,8 +21,9 @@
 //   - four warps per stream hold one query row per thread: they read S twice (the
 //     maximum, then the weights), and write P, the first half ahead of the second.
 //     The running maximum and sum stay in registers, in fp32.  P is rounded to
-//     fp16, as the products need it: 2^-11 of each weight.  O is rescaled only
-//     when a row's maximum has risen by more than 2^8: the weights are lifted to
+//     fp16, as the products need it: 2^-11 of each weight.  (The result is off by
+//     2.9e-4 of its size, rms; 2.1e-4 is its own rounding to fp16.)  O is rescaled
+//     only when a row's maximum has risen by more than 2^8: the weights are lifted to
 //     between 2^7 and 2^15 at the maximum, so that they fit fp16, and what falls
 //     below its normal range is below 2^-21 of the row's largest.
 // Segments of at most eight query rows (a sequence's own tokens, small batches)
@@ -34,14 +35,18 @@
 //
 // What bounds it (one B200; whole calls, in us, in a loop of them):
 //   - few query rows (16 sequences of 1000 .. 9000 tokens, nothing shared): HBM;
-//     307 MB take 59, of which the copies 54 (0.87 of the measured copy rate) and
-//     the start, the join and the gap between the two kernels the rest;
-//   - 512 rows per head (128 sequences behind 128k tokens): power.  A tile of 256
-//     rows takes 2930 clocks, 2048 of them tensor-core time, and the clock falls
-//     to 1.3 GHz at the 1000 W cap: 330, 0.83 PFLOP/s; started cold 250;
-//   - 256 rows (64 behind 32k): both (74), and the 19 MB of records written and
-//     read; the tensor cores are busy for a third of the tile kernel's clocks;
-//   - many short own parts (16 sequences of a multi-head layer): 46, 31 by bytes;
+//     307 MB take 59, 57.7 of them the tile kernel (0.81 of the measured copy rate);
+//   - 512 rows per head (128 sequences behind 128k tokens): a CTA takes 353 thousand
+//     clocks, in which the tensor cores are busy for 227 (a tile of 256 rows 2930, its
+//     products 2048); K and V are read once per 256 rows, twice here (1.15 GB).  Single
+//     launches take 226 at 1.6 GHz; calls 278 in a loop of 50 ms, 325 in one of seconds,
+//     where the 1000 W cap holds the clock at 1.2 .. 1.3 GHz: 0.85 PFLOP/s;
+//   - 256 rows (64 behind 32k): 64, and 70 in a loop of seconds (power cap, 1.7 GHz).
+//     82 CTAs hold prefix tiles only, bound by the products and the softmax, 65 own
+//     tiles only, which move 34 bytes per ns each (36 in the first case above), with
+//     HBM at two thirds of the copy rate;
+//   - many short own parts (16 sequences of a multi-head layer): 47, 31 by bytes; 45 CTAs
+//     hold prefix tiles, whose 16 rows take the form of 128, and 102 own tiles;
 //   - small calls (15 .. 18): latency: set-up 2, first copies 2, a tile's chain 2,
 //     the records and the join 6.
 #include <cstring>
