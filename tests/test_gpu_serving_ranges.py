@@ -159,3 +159,103 @@ def test_sizes_past_32_bits_and_bad_prefixes_are_refused():
         with pytest.raises(ValueError):
             update_page_table(lens, lens, table, free, i32([3]), **bad)
     PageTableUpdate(lens, table, free, 8, 32)(lens, i32([3]))
+
+
+def test_prefix_decode_of_nothing():
+    """No sequences; a cache without rows (refused where it has no address, as all
+    calls do); sequences that are all empty."""
+    import ctypes
+    from adaptive_top_sparse_quest_b200 import KVCache, PrefixDecodeStep, TwError, _capi, prefix_decode
+    k = torch.zeros(4, 2, PAGE, D, dtype=torch.float16, device="cuda")
+    kv = KVCache(k, k, i32([]), torch.zeros(0, 4, dtype=torch.int32, device="cuda"))
+    out, lse = prefix_decode(k.new_zeros(0, 8, D), kv, 16)
+    assert out.shape == (0, 8, D) and lse.shape == (0, 8)
+    none, q = k.new_zeros(3, 2, 0, D), torch.randn(3, 4, D, device="cuda").half()
+    with pytest.raises(TwError):
+        PrefixDecodeStep(KVCache(none, none, i32([0, 5, -1])), 4, 0)(q)
+    kv = KVCache(k[:3], k[:3], i32([0, 0, -7]))
+    step = PrefixDecodeStep(kv, 4, 0)
+    for rows in (PAGE, 0):
+        step.out.fill_(7)
+        st = kv.struct()
+        st.max_seq_len = rows
+        assert _capi.load().tw_prefix_decode(
+            q.data_ptr(), 4, ctypes.byref(st), 0, step.out.data_ptr(), step.lse.data_ptr(),
+            step.ws.data_ptr(), step.ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+        assert bool((step.out == 0).all()) and bool((step.lse == float("-inf")).all())
+
+
+@pytest.mark.parametrize("c", [
+    dict(Hq=8, Hk=1, P=16, lens=[16 + i % 5 for i in range(5000)], paged=True),
+    dict(Hq=256, Hk=128, P=48, lens=[50, 47, 300], paged=True),
+    dict(Hq=4, Hk=1, P=0, lens=[262144], paged=False),
+    dict(Hq=2, Hk=2, P=4096, lens=[4096, 4096, 1], paged=True),
+], ids=["5000", "128heads", "256k", "no_own"])
+def test_prefix_decode_at_the_ends_of_the_range(c):
+    from adaptive_top_sparse_quest_b200 import KVCache, PrefixDecodeStep, device_status
+    q, k, v, table, lens = make_prefix_case(31, c["Hq"], c["Hk"], c["P"], c["lens"], c["paged"])
+    step = PrefixDecodeStep(KVCache(k, v, lens, table), c["Hq"], c["P"])
+    step(q)
+    assert device_status(step.ws) == 0
+    check_attention(q, k, v, table, lens.tolist(), step.out, step.lse)
+
+
+def test_serving_step_captured_across_streams():
+    """A graph that forks: lengths come by a copy, the table is updated on one
+    branch while q is copied on another, rows are written and attended to after
+    both; replayed with other inputs."""
+    from adaptive_top_sparse_quest_b200 import (KVCache, PageTableUpdate, PrefixDecodeStep,
+                                                device_status, page_meta, quantize_keys, write_rows)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    B, Hq, Hk, W, P, T = 5, 16, 2, 10, 32, 60
+    pool = 2 + B * (W - 2)
+
+    def rnd(*s):
+        return torch.randn(s, generator=g, device="cuda", dtype=torch.float16)
+
+    k, v = rnd(pool, Hk, PAGE, D), rnd(pool, Hk, PAGE, D)
+    table = i32([[0, 1] + [0] * (W - 2) for _ in range(B)])
+    lens, free, nf = i32([P] * B), i32(list(range(2, pool)) + [0, 0]), i32([pool - 2])
+    kv = KVCache(k, v, lens, table)
+    keys, meta = quantize_keys(kv), page_meta(kv)
+    update = PageTableUpdate(lens, table, free, T, P, in_place=True)
+    step = PrefixDecodeStep(kv, Hq, P)
+    new, q, kn, vn = i32([P] * B), rnd(B, Hq, D), rnd(T, Hk, D), rnd(T, Hk, D)
+    h_new, h_q = new.cpu().pin_memory(), q.cpu().pin_memory()
+
+    def once(side):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            new.copy_(h_new, non_blocking=True)
+            update(new, nf)
+        q.copy_(h_q, non_blocking=True)
+        here.wait_stream(side)
+        write_rows(kv, kn, vn, update.slots, keys, meta)
+        side.wait_stream(here)
+        step(q, stream=side)
+        here.wait_stream(side)
+
+    side = torch.cuda.Stream()
+    once(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        once(side)
+    m = dict(lens=[P] * B, table=table.tolist(), free=free.tolist(), nf=int(nf))
+    for want in ([33, 40, 32, 50, 32], [34, 41, 32, 32, 60], [90, 42, 45, 33, 61], [32] * 5):
+        h_new.copy_(torch.tensor(want, dtype=torch.int32))
+        h_q.copy_(rnd(B, Hq, D).cpu())
+        kn.copy_(rnd(T, Hk, D))
+        vn.copy_(rnd(T, Hk, D))
+        graph.replay()
+        torch.cuda.synchronize()
+        ml, mnf, slots, _ = model_page_table(m["lens"], want, m["table"], m["free"], m["nf"], T, P)
+        m.update(lens=ml, nf=mnf)
+        # (the third asks for 56 + 1 + 13 + 1 + 1 of 60 places: two are served)
+        assert lens.tolist() == ml and update.slots.tolist() == slots
+        assert table.tolist() == m["table"] and device_status(step.ws) == 0
+        for i, s in enumerate(slots):
+            if s >= 0:
+                assert torch.equal(k[s // PAGE, :, s % PAGE], kn[i])
+        check_attention(h_q.cuda(), k, v, table, ml, step.out, step.lse)
